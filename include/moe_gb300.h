@@ -53,7 +53,8 @@
  *  - What only the device reads is checked there, so that no input sends a
  *    kernel outside its buffers: expert ids outside [0, E) (left out of the
  *    permutation, reported as MOE_ERR_INVALID_ARG by moe_sync_status()),
- *    combine rows outside [0, T*k) (skipped), group offsets (clamped).
+ *    combine rows outside [0, T*k) (skipped), group offsets (clamped), and
+ *    the pages, slots, rows and positions of the cache calls (see there).
  *  - The first call on each device that launches a permutation or a grouped
  *    GEMM looks up the device error word (cudaGetSymbolAddress) and sets
  *    kernel attributes; make such a call once before capturing any of them
@@ -78,6 +79,7 @@ extern "C" {
 #define MOE_ERR_WORKSPACE 3
 #define MOE_ERR_CUDA 4
 #define MOE_ERR_TIMEOUT 5
+#define MOE_ERR_PAGES 6   /* no free page was left in the key/value cache */
 
 /* ------------------------------------------------------------ data formats */
 #define MOE_FMT_BF16 0
@@ -111,9 +113,10 @@ int moe_set_wait_timeout_ns(unsigned long long ns);
 
 /* Synchronises `stream`, then returns MOE_ERR_TIMEOUT if any kernel of this
  * library recorded a wait time-out since the last call, else
- * MOE_ERR_INVALID_ARG if a permutation met an expert id outside [0, E)
- * (clearing the record either way), MOE_ERR_CUDA on a CUDA error, else
- * MOE_OK. */
+ * MOE_ERR_INVALID_ARG if a permutation met an expert id outside [0, E) or
+ * a cache call an index outside its array, else MOE_ERR_PAGES if a cache call
+ * found no free page (clearing the record in each case), MOE_ERR_CUDA on a
+ * CUDA error, else MOE_OK. */
 int moe_sync_status(void* stream);
 
 /* Test hook for the time-out path: launches one block whose thread waits on
@@ -474,6 +477,116 @@ int moe_forward_graph_create(const moe_layer* L, const uint16_t* x, const float*
                              void** graph);
 int moe_graph_launch(void* graph, void* stream);
 int moe_graph_destroy(void* graph);
+
+/* ---------------------------------------------- paged NVFP4 key/value cache
+ * The attention side of a serving step around the MoE layer: the pages name
+ * per-head QK-norm ("CuTeDSL at Perplexity", section on QK norm), the fusion
+ * of the rotation with the quantised write ("Driving vLLM WideEP ...", kernel
+ * fusion) and a heads-major KV cache ("Hosting Qwen on Blackwell").
+ *
+ * Cache: the pool of one layer is uint8 [num_pages][Hkv][record].  A record
+ * holds the page_size tokens of one page and kv head, one section after the
+ * other: key codes [page_size][D/2], key scales [page_size][D/16], value
+ * codes, value scales; page_size * D * 9 / 8 bytes.  Codes and scales are
+ * NVFP4 along D with one given fp32 global scale per kv head (g_k, g_v
+ * [Hkv]).  Token slot s lies in page s / page_size at offset s % page_size.
+ * page_size is 32, 64 or 128 and D 64 or 128.  The pool is 16-byte aligned.
+ *
+ * Sequences: table int32 [rows][max_pages] holds the page of tokens
+ * j*page_size .. of a row at j (-1: none), lens int32 [rows] the tokens, refs
+ * int32 [num_pages] (16-byte aligned) how many rows map a page (0: free).
+ * The partial last page of a row is never shared.
+ */
+
+/* Per-head RMS norms of queries and keys, the position rotation, and the
+ * write of keys and values into the cache, in one pass:
+ *   y = x * r * w,  r = 1 / sqrt(mean(x^2) + eps)   over the D values of a head
+ *   (a, b) -> (a cos - b sin, b cos + a sin)        over rot/2 pairs of y
+ * each operation rounded to fp32 and the squares summed as a binary tree over
+ * neighbours, so that every result depends on its own token alone, bit for bit.
+ *   q, k, v : bf16 [T][heads][D], *_stride elements between tokens (slices of
+ *             one projection's output; multiples of 8, 16-byte aligned)
+ *   wq, wk  : bf16 [D] or NULL (no norm)
+ *   cos_sin : fp32 [max_pos][rot], cosines then sines; rot % 16 == 0, rot <= D,
+ *             0 rotates nothing.  Pairs are (i, i + rot/2), or (2i, 2i + 1)
+ *             if `interleaved`.  pos int32 [T]; one outside [0, max_pos) is
+ *             clamped and reported by moe_sync_status().
+ *   q_out   : bf16 [T][Hq][D];  k_out : bf16 [T][Hkv][D] or NULL
+ *   pool    : the layer's pool or NULL (then v, g_k, g_v, slots are not read).
+ *             slots int64 [T]: where each token goes; negative: not written;
+ *             past the pool: not written and reported. */
+int moe_qk_norm_rope(const uint16_t* q, long long q_stride, const uint16_t* k, long long k_stride,
+                     const uint16_t* v, long long v_stride, int T, int Hq, int Hkv, int D,
+                     const uint16_t* wq, const uint16_t* wk, float eps,
+                     const float* cos_sin, int max_pos, int rot, int interleaved, const int32_t* pos,
+                     uint16_t* q_out, uint16_t* k_out,
+                     uint8_t* pool, int num_pages, int page_size, const float* g_k, const float* g_v,
+                     const long long* slots, void* stream);
+
+/* Attention of a ragged batch over the cache (keys of the new tokens already
+ * written).  Sequence b has the queries q_offsets[b] .. q_offsets[b+1] (int32
+ * [B + 1], never falling) at the last positions of its kv_lens[b] keys.  Query
+ * i sits at position p = kv_lens - n + i and sees the keys t < kv_lens, if
+ * `causal` only t <= p, if window > 0 (causal only) only t > p - window.
+ *   out[t][h] = sum_j softmax_j(scale * q . k_j) v_j;  0 where no key is seen
+ *   lse[t][h] = log sum_j exp(scale * q . k_j) (fp32 [T][Hq] or NULL), -inf there
+ * Hq % Hkv == 0; query head h reads kv head h / (Hq / Hkv).  q bf16 [T][Hq][D]
+ * with q_stride elements between tokens, out bf16 [T][Hq][D].  Rows of no
+ * sequence are not written.  Offsets that fall, lengths past the table and
+ * pages outside the pool are clamped (the last are reported).  The result of
+ * a call is the same each time, whatever the order its blocks ran in. */
+size_t moe_kv4_attention_workspace_size(int T, int B, int Hq, int Hkv, int D);
+int moe_kv4_attention(const uint16_t* q, long long q_stride, int T, int Hq,
+                      const uint8_t* pool, int num_pages, int page_size, int Hkv, int D,
+                      const float* g_k, const float* g_v,
+                      const int32_t* q_offsets, const int32_t* kv_lens, const int32_t* table, int B, int max_pages,
+                      float scale, int causal, int window, uint16_t* out, float* lse,
+                      void* ws, size_t ws_bytes, void* stream);
+
+/* Operations on pages.  Each reads *_in and writes *_out, which may be the
+ * same arrays (in place) or others (then everything is carried over).  Pages
+ * are taken lowest free id first, so the result is a function of the state.
+ * `rows` of the workspace: the table's rows, or n where that is larger. */
+size_t moe_kv_pages_workspace_size(int num_pages, int rows);
+
+/* Room for new tokens: row r gets the tokens q_offsets[r] .. q_offsets[r+1]
+ * (int32 [rows + 1]) behind its lens[r]; slots int64 [T] and pos int32 [T]
+ * are what moe_qk_norm_rope takes.  A row that finds no free page or has no
+ * room in its table row stays as it is, its slots are -1, and the failure is
+ * reported by moe_sync_status() (MOE_ERR_PAGES / MOE_ERR_INVALID_ARG). */
+int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* table_in, const int32_t* lens_in,
+                  const int32_t* refs_in, int rows, int max_pages, int num_pages, int page_size,
+                  int32_t* table_out, int32_t* lens_out, int32_t* refs_out, long long* slots, int32_t* pos,
+                  void* ws, size_t ws_bytes, void* stream);
+
+/* Row dst[i] becomes a fork of row src[i] (n pairs, int32): full pages are
+ * shared, the partial page is copied to a free one in every layer.  The pools
+ * of the layers are layer_stride bytes apart, a page is page_bytes long
+ * (layers may be 0: no copies).  dst rows must be empty and distinct; a pair
+ * that breaks this is left out and reported; without a free page the fork
+ * keeps its full pages only and MOE_ERR_PAGES is reported. */
+int moe_kv_fork(const int32_t* src, const int32_t* dst, int n, const int32_t* table_in, const int32_t* lens_in,
+                const int32_t* refs_in, int rows, int max_pages, int num_pages, int page_size,
+                int32_t* table_out, int32_t* lens_out, int32_t* refs_out, uint8_t* pool, int layers,
+                long long layer_stride, long long page_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/* Rows rows_to_free[0..n) (int32; one listed twice is freed once) become
+ * empty; their pages are free where no other row maps them. */
+int moe_kv_free(const int32_t* rows_to_free, int n, const int32_t* table_in, const int32_t* lens_in,
+                const int32_t* refs_in, int rows, int max_pages, int num_pages, int page_size,
+                int32_t* table_out, int32_t* lens_out, int32_t* refs_out, void* stream);
+
+/* Moves the pages so that those in use are the lowest ids: the pages past
+ * their number go, in order, to the free ids below it.  remap int32
+ * [num_pages]: the new id of each page, -1 if it was free. */
+int moe_kv_compact(const int32_t* table_in, const int32_t* refs_in, int rows, int max_pages, int num_pages,
+                   int32_t* table_out, int32_t* refs_out, int32_t* remap, uint8_t* pool, int layers,
+                   long long layer_stride, long long page_bytes, void* ws, size_t ws_bytes, void* stream);
+
+/* Copies page src[i] to page dst[i] in every layer (n pairs, int32).  No page
+ * may be a destination and appear a second time in either list. */
+int moe_kv_copy_pages(uint8_t* pool, int layers, long long layer_stride, long long page_bytes, int num_pages,
+                      const int32_t* src, const int32_t* dst, int n, void* stream);
 
 #ifdef __cplusplus
 }

@@ -12,7 +12,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "lib", "libmoe_gb300.so")
 
 c_int, c_size_t, c_void_p, c_float = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
-c_ull = ctypes.c_ulonglong
+c_ull, c_ll = ctypes.c_ulonglong, ctypes.c_longlong
 
 MOE_OK = 0
 MOE_ERR_INVALID_ARG = 1
@@ -20,6 +20,7 @@ MOE_ERR_UNSUPPORTED = 2
 MOE_ERR_WORKSPACE = 3
 MOE_ERR_CUDA = 4
 MOE_ERR_TIMEOUT = 5
+MOE_ERR_PAGES = 6
 
 MOE_FMT_BF16 = 0
 MOE_FMT_NVFP4 = 1
@@ -93,6 +94,23 @@ SIGNATURES = {
                                          c_void_p, c_size_t, c_void_p, ctypes.POINTER(c_void_p)]),
     "moe_graph_launch": (c_int, [c_void_p, c_void_p]),
     "moe_graph_destroy": (c_int, [c_void_p]),
+    "moe_qk_norm_rope": (c_int, [c_void_p, c_ll, c_void_p, c_ll, c_void_p, c_ll, c_int, c_int, c_int, c_int,
+                                 c_void_p, c_void_p, c_float, c_void_p, c_int, c_int, c_int, c_void_p,
+                                 c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_kv4_attention_workspace_size": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "moe_kv4_attention": (c_int, [c_void_p, c_ll, c_int, c_int, c_void_p, c_int, c_int, c_int, c_int,
+                                  c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
+                                  c_float, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_kv_pages_workspace_size": (c_size_t, [c_int, c_int]),
+    "moe_kv_extend": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                              c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "moe_kv_fork": (c_int, [c_void_p, c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                            c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_ll, c_ll, c_void_p, c_size_t, c_void_p]),
+    "moe_kv_free": (c_int, [c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                            c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_kv_compact": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_void_p,
+                               c_int, c_ll, c_ll, c_void_p, c_size_t, c_void_p]),
+    "moe_kv_copy_pages": (c_int, [c_void_p, c_int, c_ll, c_ll, c_int, c_void_p, c_void_p, c_int, c_void_p]),
 }
 
 _lib = None

@@ -480,13 +480,282 @@ def moe_forward_host_pipelined(layer_c, x_host, logits_host, out_host, x_dev: to
     return out_host
 
 
+def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
+    """An output or scratch tensor from the memory of the stream that will
+    write it (another stream's free blocks may still be in use there)."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _heads(t: torch.Tensor, name: str, T=None, D=None, device=None) -> None:
+    """bf16 [T, heads, D] whose tokens may be apart (a slice of a projection's
+    output): heads and D contiguous, any token stride."""
+    if t is None:
+        raise ValueError(f"{name}: required")
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [T, heads, D]")
+    s, h, d = t.stride(), t.shape[1], t.shape[2]
+    if (d > 1 and s[2] != 1) or (h > 1 and s[1] != d):
+        raise ValueError(f"{name}: heads must be contiguous within a token")
+    if T is not None and t.shape[0] != T:
+        raise ValueError(f"{name}: expected {T} tokens, got {t.shape[0]}")
+    if D is not None and d != D:
+        raise ValueError(f"{name}: expected head size {D}, got {d}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _pool_page_size(pool: torch.Tensor, Hkv: int, D: int, device) -> int:
+    """The page size of a layer's pool uint8 [num_pages, Hkv, page_size*D*9/8]."""
+    _dev(pool, "pool", dtype=torch.uint8, device=device)
+    if pool.dim() != 3 or pool.shape[1] != Hkv or pool.shape[2] * 8 % (9 * D):
+        raise ValueError(f"pool: expected [num_pages, {Hkv}, page_size * {D} * 9 / 8], got {tuple(pool.shape)}")
+    return pool.shape[2] * 8 // (9 * D)
+
+
+def moe_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: Optional[torch.Tensor] = None,
+                     pos: Optional[torch.Tensor] = None, wq: Optional[torch.Tensor] = None,
+                     wk: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                     v: Optional[torch.Tensor] = None, pool: Optional[torch.Tensor] = None,
+                     g_k: Optional[torch.Tensor] = None, g_v: Optional[torch.Tensor] = None,
+                     slots: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                     k_out: Optional[torch.Tensor] = None, stream=None):
+    """Per-head RMS norms of q and k, the rotation, and the NVFP4 write of k and
+    v into the cache (see include/moe_gb300.h).  q bf16 [T, Hq, D], k and v
+    bf16 [T, Hkv, D] (any token stride); wq / wk bf16 [D] or None; cos_sin fp32
+    [max_pos, rot] with pos int32 [T], or None for no rotation; pool uint8
+    [num_pages, Hkv, record] with g_k, g_v fp32 [Hkv] and slots int64 [T].
+    Returns (q_out, k_out); k_out is allocated only where there is no pool."""
+    _heads(q, "q")
+    T, Hq, D = q.shape
+    dev = q.device
+    _heads(k, "k", T, D, dev)
+    Hkv = k.shape[1]
+    _opt(wq, "wq", dtype=torch.bfloat16, shape=(D,), device=dev)
+    _opt(wk, "wk", dtype=torch.bfloat16, shape=(D,), device=dev)
+    rot = max_pos = num_pages = page_size = v_stride = 0
+    if cos_sin is not None:
+        _dev(cos_sin, "cos_sin", dtype=torch.float32, device=dev)
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin: expected [max_pos, rot]")
+        max_pos, rot = cos_sin.shape
+        _dev(pos, "pos", dtype=torch.int32, shape=(T,), device=dev)
+    if pool is not None:
+        page_size, num_pages = _pool_page_size(pool, Hkv, D, dev), pool.shape[0]
+        _heads(v, "v", T, D, dev)
+        if v.shape[1] != Hkv:
+            raise ValueError(f"v: expected {Hkv} heads, got {v.shape[1]}")
+        v_stride = _token_stride(v)
+        _dev(g_k, "g_k", dtype=torch.float32, shape=(Hkv,), device=dev)
+        _dev(g_v, "g_v", dtype=torch.float32, shape=(Hkv,), device=dev)
+        _dev(slots, "slots", dtype=torch.int64, shape=(T,), device=dev)
+    if q_out is None:
+        q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+    else:
+        _dev(q_out, "q_out", dtype=torch.bfloat16, shape=(T, Hq, D), device=dev)
+    if k_out is None and pool is None:
+        k_out = _empty((T, Hkv, D), torch.bfloat16, dev, stream)
+    elif k_out is not None:
+        _dev(k_out, "k_out", dtype=torch.bfloat16, shape=(T, Hkv, D), device=dev)
+    check(load().moe_qk_norm_rope(_ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), v_stride, T, Hq, Hkv,
+                                  D, _ptr(wq), _ptr(wk), eps, _ptr(cos_sin), max_pos, rot, int(interleaved),
+                                  _ptr(pos), _ptr(q_out), _ptr(k_out), _ptr(pool), num_pages, page_size, _ptr(g_k),
+                                  _ptr(g_v), _ptr(slots), _stream(stream)), "moe_qk_norm_rope")
+    return q_out, k_out
+
+
+def moe_kv4_attention(q: torch.Tensor, pool: torch.Tensor, g_k: torch.Tensor, g_v: torch.Tensor,
+                      q_offsets: torch.Tensor, kv_lens: torch.Tensor, table: torch.Tensor,
+                      scale: Optional[float] = None, causal: bool = True, window: int = 0,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Attention of a ragged batch over the paged NVFP4 cache (see
+    include/moe_gb300.h).  q bf16 [T, Hq, D] (any token stride), pool uint8
+    [num_pages, Hkv, record], q_offsets int32 [B + 1], kv_lens int32 [B],
+    table int32 [B, max_pages]; scale defaults to D ** -0.5; lse fp32 [T, Hq]
+    is written where given.  Returns out bf16 [T, Hq, D]."""
+    _heads(q, "q")
+    T, Hq, D = q.shape
+    dev = q.device
+    _dev(g_k, "g_k", dtype=torch.float32, device=dev)
+    Hkv = g_k.numel()
+    _dev(g_v, "g_v", dtype=torch.float32, shape=(Hkv,), device=dev)
+    page_size = _pool_page_size(pool, Hkv, D, dev)
+    _dev(table, "table", dtype=torch.int32, device=dev)
+    if table.dim() != 2:
+        raise ValueError("table: expected [B, max_pages]")
+    B, max_pages = table.shape
+    _dev(q_offsets, "q_offsets", dtype=torch.int32, shape=(B + 1,), device=dev)
+    _dev(kv_lens, "kv_lens", dtype=torch.int32, shape=(B,), device=dev)
+    if out is None:
+        out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
+    else:
+        _dev(out, "out", dtype=torch.bfloat16, shape=(T, Hq, D), device=dev)
+    _opt(lse, "lse", dtype=torch.float32, shape=(T, Hq), device=dev)
+    lib = load()
+    if ws is None:
+        ws = _empty(lib.moe_kv4_attention_workspace_size(T, B, Hq, Hkv, D), torch.uint8, dev, stream)
+    else:
+        _dev(ws, "ws", device=dev)
+    check(lib.moe_kv4_attention(_ptr(q), _token_stride(q), T, Hq, _ptr(pool), pool.shape[0], page_size, Hkv, D,
+                                _ptr(g_k), _ptr(g_v), _ptr(q_offsets), _ptr(kv_lens), _ptr(table), B, max_pages,
+                                D ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), _ptr(lse),
+                                _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_kv4_attention")
+    return out
+
+
+def _kv_state(table, refs, lens=None):
+    """Checks the arrays of the page operations; returns rows, max_pages, num_pages."""
+    _dev(table, "table", dtype=torch.int32)
+    if table.dim() != 2:
+        raise ValueError("table: expected [rows, max_pages]")
+    _dev(refs, "refs", dtype=torch.int32, device=table.device)
+    if refs.dim() != 1:
+        raise ValueError("refs: expected [num_pages]")
+    if lens is not None:
+        _dev(lens, "lens", dtype=torch.int32, shape=(table.shape[0],), device=table.device)
+    return table.shape[0], table.shape[1], refs.numel()
+
+
+def _kv_pools(pool: Optional[torch.Tensor], num_pages: int, device):
+    """(pointer, layers, bytes between layers, bytes of a page) of uint8 [layers, num_pages, ...] or None."""
+    if pool is None:
+        return None, 0, 0, 16
+    _dev(pool, "pool", dtype=torch.uint8, device=device)
+    if pool.dim() < 3 or pool.shape[1] != num_pages:
+        raise ValueError(f"pool: expected [layers, {num_pages}, ...], got {tuple(pool.shape)}")
+    page = pool[0, 0].numel() if pool.shape[0] and num_pages else 16
+    return pool.data_ptr(), pool.shape[0], page * num_pages, page
+
+
+def _index(t: torch.Tensor, name: str, device) -> int:
+    _dev(t, name, dtype=torch.int32, device=device)
+    if t.dim() != 1:
+        raise ValueError(f"{name}: expected one dimension")
+    return t.numel()
+
+
+def _like(out, name, t, inplace, stream):
+    """The output of a page operation: the given one, the input in place, or a new one."""
+    if out is not None:
+        _dev(out, name, dtype=t.dtype, shape=t.shape, device=t.device)
+        return out
+    return t if inplace else _empty(t.shape, t.dtype, t.device, stream)
+
+
+def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                  page_size: int, inplace: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """Room for new tokens: row r gets tokens q_offsets[r] .. q_offsets[r+1]
+    (int32 [rows + 1], T tokens in all).  Returns dict(table, lens, refs,
+    slots int64 [T], pos int32 [T]); inplace=True writes the state back into
+    the arguments, `out` may hold any of the outputs."""
+    S, M, N = _kv_state(table, refs, lens)
+    dev = table.device
+    _dev(q_offsets, "q_offsets", dtype=torch.int32, shape=(S + 1,), device=dev)
+    o = out or {}
+    r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
+             lens=_like(o.get("lens"), "lens", lens, inplace, stream),
+             refs=_like(o.get("refs"), "refs", refs, inplace, stream), slots=o.get("slots"), pos=o.get("pos"))
+    for name, dt in (("slots", torch.int64), ("pos", torch.int32)):
+        if r[name] is None:
+            r[name] = _empty((T,), dt, dev, stream)
+        else:
+            _dev(r[name], name, dtype=dt, shape=(T,), device=dev)
+    lib = load()
+    ws = _empty(lib.moe_kv_pages_workspace_size(N, S), torch.uint8, dev, stream)
+    check(lib.moe_kv_extend(_ptr(q_offsets), T, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
+                            _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _ptr(r["slots"]), _ptr(r["pos"]),
+                            _ptr(ws), ws.numel(), _stream(stream)), "moe_kv_extend")
+    return r
+
+
+def moe_kv_fork(src: torch.Tensor, dst: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                pool: Optional[torch.Tensor] = None, page_size: int = 64, inplace: bool = False,
+                out: Optional[dict] = None, stream=None) -> dict:
+    """Rows dst (empty, distinct) become forks of rows src (int32 [n] both).
+    pool uint8 [layers, num_pages, ...] gets the copies of the partial pages.
+    Returns dict(table, lens, refs)."""
+    S, M, N = _kv_state(table, refs, lens)
+    dev = table.device
+    n = _index(src, "src", dev)
+    if _index(dst, "dst", dev) != n:
+        raise ValueError("dst: expected as many rows as src")
+    base, layers, layer_stride, page_bytes = _kv_pools(pool, N, dev)
+    o = out or {}
+    r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
+             lens=_like(o.get("lens"), "lens", lens, inplace, stream),
+             refs=_like(o.get("refs"), "refs", refs, inplace, stream))
+    lib = load()
+    ws = _empty(lib.moe_kv_pages_workspace_size(N, max(S, n)), torch.uint8, dev, stream)
+    check(lib.moe_kv_fork(_ptr(src), _ptr(dst), n, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
+                          _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), base, layers, layer_stride, page_bytes,
+                          _ptr(ws), ws.numel(), _stream(stream)), "moe_kv_fork")
+    return r
+
+
+def moe_kv_free(rows: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, page_size: int = 64,
+                inplace: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """Rows (int32 [n]) become empty.  Returns dict(table, lens, refs)."""
+    S, M, N = _kv_state(table, refs, lens)
+    n = _index(rows, "rows", table.device)
+    o = out or {}
+    r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
+             lens=_like(o.get("lens"), "lens", lens, inplace, stream),
+             refs=_like(o.get("refs"), "refs", refs, inplace, stream))
+    check(load().moe_kv_free(_ptr(rows), n, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
+                             _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _stream(stream)), "moe_kv_free")
+    return r
+
+
+def moe_kv_compact(table: torch.Tensor, refs: torch.Tensor, pool: Optional[torch.Tensor] = None,
+                   inplace: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """Moves the pages in use to the lowest ids (in pool uint8 [layers,
+    num_pages, ...] too).  Returns dict(table, refs, remap int32 [num_pages])."""
+    S, M, N = _kv_state(table, refs)
+    dev = table.device
+    base, layers, layer_stride, page_bytes = _kv_pools(pool, N, dev)
+    o = out or {}
+    r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
+             refs=_like(o.get("refs"), "refs", refs, inplace, stream), remap=_like(o.get("remap"), "remap", refs, False, stream))
+    lib = load()
+    ws = _empty(lib.moe_kv_pages_workspace_size(N, 0), torch.uint8, dev, stream)
+    check(lib.moe_kv_compact(_ptr(table), _ptr(refs), S, M, N, _ptr(r["table"]), _ptr(r["refs"]), _ptr(r["remap"]),
+                             base, layers, layer_stride, page_bytes, _ptr(ws), ws.numel(), _stream(stream)),
+          "moe_kv_compact")
+    return r
+
+
+def moe_kv_copy_pages(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, stream=None) -> torch.Tensor:
+    """Copies pages src to pages dst (int32 [n]) in every layer of pool uint8 [layers, num_pages, ...]."""
+    if pool is None or not isinstance(pool, torch.Tensor) or not pool.is_cuda or pool.dim() < 3:
+        raise ValueError("pool: expected a CUDA tensor [layers, num_pages, ...]")
+    base, layers, layer_stride, page_bytes = _kv_pools(pool, pool.shape[1], pool.device)
+    n = _index(src, "src", pool.device)
+    if _index(dst, "dst", pool.device) != n:
+        raise ValueError("dst: expected as many pages as src")
+    check(load().moe_kv_copy_pages(base, layers, layer_stride, page_bytes, pool.shape[1], _ptr(src), _ptr(dst), n,
+                                   _stream(stream)), "moe_kv_copy_pages")
+    return pool
+
+
 __all__ = ["MOE_FMT_BF16", "MOE_FMT_NVFP4", "MOE_FMT_MXFP8", "MOE_FMT_MXFP4", "moe_quant_mx", "MOE_EPI_STORE_BF16", "MOE_EPI_SWIGLU_BF16",
            "MOE_EPI_SWIGLU_NVFP4", "moe_version", "moe_sync_status", "moe_set_wait_timeout_ns",
            "moe_selftest_wait_timeout", "moe_selftest_grid_barrier_timeout", "moe_route", "moe_permute",
            "moe_route_permute", "moe_quant_nvfp4", "MOE_EPI_SWIGLU_MX",
            "moe_permute_noalloc", "moe_grouped_gemm", "moe_combine", "moe_shared_gate",
            "moe_forward_workspace_size", "moe_forward", "moe_forward_profiled", "moe_forward_host",
-           "moe_forward_host_pipelined",
+           "moe_forward_host_pipelined", "moe_qk_norm_rope", "moe_kv4_attention", "moe_kv_extend", "moe_kv_fork",
+           "moe_kv_free", "moe_kv_compact", "moe_kv_copy_pages",
            "ForwardGraph"]
 
 

@@ -169,6 +169,7 @@ const char* moe_status_string(int status) {
     case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
     case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
     case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
+    case MOE_ERR_PAGES: return "MOE_ERR_PAGES";
     default: return "MOE_ERR_UNKNOWN";
   }
 }
@@ -199,7 +200,7 @@ int moe_sync_status(void* stream) {
       set_cuda_error(e);
       return MOE_ERR_CUDA;
     }
-    return (v & kErrTimeout) ? MOE_ERR_TIMEOUT : MOE_ERR_INVALID_ARG;
+    return (v & kErrTimeout) ? MOE_ERR_TIMEOUT : (v & kErrBadIndex) ? MOE_ERR_INVALID_ARG : MOE_ERR_PAGES;
   }
   return MOE_OK;
 }

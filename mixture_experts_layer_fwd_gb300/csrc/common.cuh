@@ -120,9 +120,12 @@ DEVINL bool mbar_try_wait_suspend(uint64_t* bar, uint32_t parity, uint32_t hint_
 
 // Error word bits (device side).  The host maps kErrTimeout to
 // MOE_ERR_TIMEOUT and kErrBadIndex (an expert id outside [0, E) met by the
-// permutation, which then leaves that slot out) to MOE_ERR_INVALID_ARG.
+// permutation, which then leaves that slot out; a page, slot, row or position
+// outside its array met by the cache calls) to MOE_ERR_INVALID_ARG, and
+// kErrNoPages (no free cache page was left) to MOE_ERR_PAGES.
 constexpr unsigned int kErrTimeout = 1u;
 constexpr unsigned int kErrBadIndex = 2u;
+constexpr unsigned int kErrNoPages = 4u;
 
 // Bounded wait on an mbarrier phase.  Gives up after `timeout_ns` of wall
 // time (or as soon as *abort is set by another role of the block), records
@@ -181,6 +184,14 @@ DEVINL void tma_load_4d(const void* tmap, uint64_t* bar, void* smem_dst, int x, 
       "[%2];" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
+}
+// Untiled bulk copy of `bytes` (a multiple of 16) from global to shared
+// memory, both 16-byte aligned.
+DEVINL void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
 }
 DEVINL void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 

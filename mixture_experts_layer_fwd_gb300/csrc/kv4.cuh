@@ -1,0 +1,26 @@
+// The paged NVFP4 key/value cache: layout of a record and the helpers that
+// every kernel on it shares.
+//
+// A layer's pool is [num_pages][Hkv] records.  One record holds `P` tokens of
+// one kv head: key codes [P][D/2], key scales [P][D/16], value codes, value
+// scales, one after the other (P * D * 9/8 bytes).  Records are contiguous so
+// that one bulk copy brings everything an attention step needs of a page and
+// head into shared memory, and a page of a layer is one contiguous block.
+// P % 16 == 0 and D in {64, 128} make every section start on a 16-byte
+// boundary and the record a multiple of 16 bytes.
+#pragma once
+
+#include "nvfp4.cuh"
+
+namespace moe {
+namespace kv4 {
+
+__host__ __device__ constexpr int codes_bytes(int P, int D) { return P * D / 2; }
+__host__ __device__ constexpr int scale_bytes(int P, int D) { return P * D / 16; }
+__host__ __device__ constexpr int record_bytes(int P, int D) { return 2 * (codes_bytes(P, D) + scale_bytes(P, D)); }
+
+inline bool page_size_ok(int P) { return P == 32 || P == 64 || P == 128; }
+inline bool head_dim_ok(int D) { return D == 64 || D == 128; }
+
+}  // namespace kv4
+}  // namespace moe
