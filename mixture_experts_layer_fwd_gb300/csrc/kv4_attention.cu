@@ -546,16 +546,24 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
     }
     set[dev] = smem;
   }
-  attn_plan_kernel<kRows><<<1, 1024, 0, s>>>(p, p.P);
-  MOE_TRY(check_launch());
   attn_rows16_kernel<D><<<p.blocks, kThreads, smem, s>>>(p, stages);
+  return check_launch();
+}
+
+// Schedule, main kernel, joining.
+template <int ROWS, int D>
+int run(const AttnParams& p, int unit, cudaStream_t s) {
+  attn_plan_kernel<ROWS><<<1, 1024, 0, s>>>(p, unit);
   MOE_TRY(check_launch());
+  MOE_TRY(ROWS == kRows ? launch_rows16<D>(p, s) : attention_tiles(p, D, s));
   if (p.blocks > 1) {
-    attn_join_kernel<kRows, D><<<dim3(p.blocks - 1, 4), 128, 0, s>>>(p, p.P);
+    attn_join_kernel<ROWS, D><<<dim3(p.blocks - 1, ROWS == kRows ? 4 : 16), 128, 0, s>>>(p, unit);
     MOE_TRY(check_launch());
   }
   return MOE_OK;
 }
+
+constexpr int kTileRows = 256, kTileKeys = 128;
 
 struct Layout {
   int rows, blocks;
@@ -565,8 +573,10 @@ struct Layout {
 // Kernel variant, its blocks, and the workspace they need; fills p's pointers.
 Layout layout(AttnParams& p, int D, void* ws) {
   Layout r;
-  r.rows = kRows;
-  r.blocks = 2 * num_sms();
+  // Up to 32 rows per sequence and kv head on average: 16 rows at a time.
+  const bool tiles16 = static_cast<long long>(p.T) * p.G <= 32ll * p.B;
+  r.rows = tiles16 ? kRows : kTileRows;
+  r.blocks = tiles16 ? 2 * num_sms() : num_sms();
   Carve c(ws, 0);
   const long long tiles = static_cast<long long>(p.T) * p.G / r.rows + p.B + 1;
   p.starts = c.take<int>(p.B + 1);
@@ -575,15 +585,16 @@ Layout layout(AttnParams& p, int D, void* ws) {
   p.part_ml = c.take<float>(static_cast<size_t>(2) * r.blocks * 2 * r.rows);
   p.part_o = c.take<float>(static_cast<size_t>(2) * r.blocks * r.rows * D);
   p.blocks = r.blocks;
-  p.min_units = 1;
+  p.min_units = tiles16 ? 1 : 2;
   r.bytes = c.used;
   return r;
 }
 
 }  // namespace
 
-int attention_rows16(const AttnParams& p, int D, cudaStream_t s) {
-  return D == 128 ? launch_rows16<128>(p, s) : launch_rows16<64>(p, s);
+int attention(const AttnParams& p, int D, int rows, cudaStream_t s) {
+  if (rows == kRows) return D == 128 ? run<kRows, 128>(p, p.P, s) : run<kRows, 64>(p, p.P, s);
+  return D == 128 ? run<kTileRows, 128>(p, kTileKeys, s) : run<kTileRows, 64>(p, kTileKeys, s);
 }
 
 }  // namespace kv4
@@ -622,6 +633,7 @@ extern "C" int moe_kv4_attention(const uint16_t* q, long long q_stride, int T, i
   p.timeout_ns = wait_timeout_ns();
   p.err = device_error_word();
   if (!p.err) return MOE_ERR_CUDA;
-  if (kv4::layout(p, D, ws).bytes > ws_bytes) return MOE_ERR_WORKSPACE;
-  return kv4::attention_rows16(p, D, static_cast<cudaStream_t>(stream));
+  const kv4::Layout l = kv4::layout(p, D, ws);
+  if (l.bytes > ws_bytes) return MOE_ERR_WORKSPACE;
+  return kv4::attention(p, D, l.rows, static_cast<cudaStream_t>(stream));
 }

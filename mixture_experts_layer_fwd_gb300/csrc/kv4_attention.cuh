@@ -154,8 +154,8 @@ DEVINL long long range_of(const AttnParams& p, long long total) {
   return r < p.min_units ? p.min_units : r;
 }
 
-// Both kernels behind moe_kv4_attention: fills the schedule, runs, joins.
-int attention_rows16(const AttnParams& p, int D, cudaStream_t s);
+// Main kernel over 256-row tiles and 128-key units (kv4_prefill.cu).
+int attention_tiles(const AttnParams& p, int D, cudaStream_t s);
 
 }  // namespace kv4
 }  // namespace moe
