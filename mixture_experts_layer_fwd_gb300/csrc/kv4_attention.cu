@@ -16,7 +16,7 @@
 //
 // Codes times block scales are exact in fp16.  Q (bf16) is scaled per row by
 // a power of two into fp16's range, exact for values within 2^-29 of the
-// row's largest; P <= 1 is rounded to fp16 (2^-12); all sums are fp32.  The
+// row's largest; P is rounded to fp16 (2^-12); all sums are fp32.  The
 // global scales and Q's power of two go into the softmax scale and the output.
 #include "kv4_attention.cuh"
 
@@ -24,7 +24,7 @@ namespace moe {
 namespace kv4 {
 namespace {
 
-constexpr int kRows = 16;
+constexpr int kRows = kRowsSmall;
 constexpr int kWarps = 4;                      // consumer warps
 constexpr int kThreads = 32 * (kWarps + 1);    // and a producer warp
 constexpr int kMaxStages = 16;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, int 
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (D / 64);
 #pragma unroll
     for (int v = 0; v < D / 64; ++v) dst[v] = w[v];
-    if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l)) * (1.0f / kLog2e) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - p_shift(ROWS)) * (1.0f / kLog2e) : -INFINITY;
   }
 }
 
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
           corr[half] = ex2(m[half] - base);
           m[half] = mn;
           l[half] *= corr[half];
-          top[half] = base;
+          top[half] = base - p_shift(kRows);
         }
         uint32_t pa[2][4];
 #pragma unroll
@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
         const float inv = ll > 0.0f ? __ldg(p.g_v + c.h) / ll : 0.0f;
         *reinterpret_cast<uint2*>(p.out + row * D + 4 * q) =
             make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (p.lse && q == 0) p.lse[row] = ll > 0.0f ? (mm + log2f(ll)) * (1.0f / kLog2e) : -INFINITY;
+        if (p.lse && q == 0) p.lse[row] = ll > 0.0f ? (mm + log2f(ll) - p_shift(kRows)) * (1.0f / kLog2e) : -INFINITY;
       } else {
         *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D + 4 * q) = a;
         if (q == 0) {
@@ -563,7 +563,7 @@ int run(const AttnParams& p, int unit, cudaStream_t s) {
   return MOE_OK;
 }
 
-constexpr int kTileRows = 256, kTileKeys = 128;
+constexpr int kTileRows = kRowsTile, kTileKeys = 128;
 
 struct Layout {
   int rows, blocks;

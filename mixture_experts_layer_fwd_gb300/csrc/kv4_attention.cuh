@@ -17,6 +17,15 @@
 namespace moe {
 namespace kv4 {
 
+// P is held as p * 2^shift in fp16, p the weight relative to the running
+// maximum: normal numbers reach down to 2^(-14-shift), and what is lost below
+// is at most 2^(-25-shift) per key.  The largest value is 2^15: the 16-row
+// kernel's maximum is exact, the 256-row kernel's lags by up to 2^8.  The sums
+// and O carry the factor too, so it cancels except in the log of the sum.
+constexpr int kRowsSmall = 16, kRowsTile = 256;
+constexpr float kSlack = 8.0f;
+__host__ __device__ constexpr float p_shift(int rows) { return rows == kRowsSmall ? 15.0f : 15.0f - kSlack; }
+
 struct AttnParams {
   const uint16_t* q;  // bf16 [T][Hq][D], q_stride elements between tokens
   long long q_stride;

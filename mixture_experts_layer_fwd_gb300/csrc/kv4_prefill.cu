@@ -18,8 +18,8 @@
 // one tile's softmax runs under the other's products.  S and O fill tensor
 // memory: 2 x 128 + 2 x D columns; P lies in the first half of its S.
 //
-// The running maximum is moved only when a row's grows by more than 2^8: until
-// then P <= 2^8 and O needs no rescaling, which is exact up to fp16's range.
+// The running maximum is moved only when a row's grows by more than 2^kSlack:
+// until then O needs no rescaling, and P keeps fp16's relative precision.
 // Numbers are as in the 16-row kernel: codes times block scales and Q times a
 // power of two are exact in fp16, P is rounded to fp16, sums are fp32.
 #include "kv4_attention.cuh"
@@ -28,12 +28,11 @@ namespace moe {
 namespace kv4 {
 namespace {
 
-constexpr int kRows = 256;
+constexpr int kRows = kRowsTile;
 constexpr int kKeys = 128;
 constexpr int kThreads = 512;
 constexpr int kMaxSlots = 16;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kSlack = 8.0f;  // log2 of the most that P may exceed 1
 constexpr int kExpand0 = 8, kLoad = 12, kMma = 13, kWait = 14;
 
 template <int D>
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           int lo = 0, hi = c.s.len;  // a row that is not there masks nothing
           const bool have = idx < c.s.n * p.G;
           if (have) row_keys(p, c.s, idx / p.G, lo, hi);
-          float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units) and its negative (0 for none)
+          float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units); P's shift less it (0 for none)
           uint64_t l2[2] = {0ull, 0ull};
           for (int i = 0; i < n; ++i, ++cnt) {
             mbar_wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, &bars.abort);
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               if (grow) {
                 f = m == -INFINITY ? 0.0f : ex2(m - top);
                 m = top;
-                nb = -top;
+                nb = p_shift(kRows) - top;
               }
               const uint64_t ff = pair(f, f);
 #pragma unroll
@@ -355,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 }
               }
             }
-            if (p.lse && have) p.lse[row] = l > 0.0f ? (m + log2f(l)) * (1.0f / kLog2e) : -INFINITY;
+            if (p.lse && have) p.lse[row] = l > 0.0f ? (m + log2f(l) - p_shift(kRows)) * (1.0f / kLog2e) : -INFINITY;
           } else {
             const long long slot = 2ll * blockIdx.x + (c.u == c.u0 ? 1 : 0);
             const int rr = g * 128 + r;
