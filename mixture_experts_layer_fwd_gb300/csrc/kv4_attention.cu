@@ -25,10 +25,11 @@ namespace kv4 {
 namespace {
 
 constexpr int kRows = kRowsSmall;
-constexpr int kWarps = 4;                      // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);    // and a producer warp
+constexpr int kWarps = 4;     // consumer warps of a group
+constexpr int kGroups = 3;    // groups of a block, each with its own range of the work
+constexpr int kThreads = 32 * kGroups * kWarps + 128;  // and a warpgroup with their producers
 constexpr int kMaxStages = 16;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSmem = 226 * 1024;
 
 // ------------------------------------------------------------------ schedule
 template <int ROWS>
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, int 
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (D / 64);
 #pragma unroll
     for (int v = 0; v < D / 64; ++v) dst[v] = w[v];
-    if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - p_shift(ROWS)) * (1.0f / kLog2e) : -INFINITY;
+    if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
   }
 }
 
@@ -163,54 +164,31 @@ DEVINL void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Four bytes of E2M1 pairs -> four fp16 pairs (low nibble first).
-DEVINL void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-// 2^x by the hardware's approximation (2 ulp), 0 for -infinity
-DEVINL float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-DEVINL uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
+// One group's shared memory beside its ring: 4 consumer warps share it.
 template <int D>
-struct Shared {
+struct Group {
   uint64_t full[kMaxStages], empty[kMaxStages];
   float m[kWarps][kRows], l[kWarps][kRows];
   int abort;
-  alignas(16) float o[kWarps][kRows][D];
+  alignas(16) float o[kWarps][kRows][D / 2];  // half the columns at a time
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams p, int stages) {
+__global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnParams p, int stages) {
   constexpr int KS = D / 16;  // k steps of S
   constexpr int LD = D / 4;   // values of a key per lane (S), of a row of O per lane
   constexpr int NT = D / 8;   // column tiles of O
+  constexpr int W = D / 64;   // words of a value row per lane
   extern __shared__ __align__(128) uint8_t smem[];
-  Shared<D>& sh = *reinterpret_cast<Shared<D>*>(smem);
-  uint8_t* ring = smem + ((sizeof(Shared<D>) + 127) & ~size_t(127));
   const int rec = record_bytes(p.P, D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int grp = warp < kGroups * kWarps ? warp / kWarps : warp - kGroups * kWarps;
+  constexpr int head = (sizeof(Group<D>) + 127) & ~127;
+  uint8_t* mine = smem + min(grp, kGroups - 1) * (head + stages * rec);
+  Group<D>& sh = *reinterpret_cast<Group<D>*>(mine);
+  uint8_t* ring = mine + head;
 
-  if (threadIdx.x == 0) {
+  if (warp < kGroups * kWarps && warp % kWarps == 0 && lane == 0) {
     for (int i = 0; i < stages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
@@ -220,12 +198,14 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
   }
   __syncthreads();
 
+  const int block = blockIdx.x * kGroups + grp;  // the group's range
   const long long total = total_units(p), range = range_of(p, total);
-  const long long x0 = blockIdx.x * range, x1 = min(total, x0 + range);
-  if (x0 >= x1) return;
+  const long long x0 = block * range, x1 = min(total, x0 + range);
 
-  if (warp == kWarps) {
-    // -------- producer: one page record per stage
+  if (warp >= kGroups * kWarps) {
+    // -------- producers, one per group: one page record per stage
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
+    if (grp >= kGroups || x0 >= x1) return;
     Cursor c = cursor_at<kRows>(p, p.P, x0);
     uint32_t it = 0;
     long long left = x1 - x0;
@@ -233,10 +213,10 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
       const int n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
       const int32_t* row = p.table + static_cast<long long>(c.b) * p.max_pages + c.u;
       for (int base = 0; base < n; base += 32) {
-        const int mine = base + lane;
+        const int at = base + lane;
         int page = -1;
-        if (mine < n && (c.u + mine) * p.P < c.s.len) {
-          page = __ldg(row + mine);
+        if (at < n && (c.u + at) * p.P < c.s.len) {
+          page = __ldg(row + at);
           if (page < 0 || page >= p.num_pages) {
             atomicOr(p.err, kErrBadIndex);
             page = 0;
@@ -248,8 +228,8 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
           const int st = it % stages;
           if (lane == 0) {
             if (it >= static_cast<uint32_t>(stages))
-              mbar_wait_bounded(&sh.empty[st], (it / stages - 1) & 1, p.timeout_ns, p.err, &sh.abort);
-            if (pg < 0 || sh.abort) {
+              mbar_wait_bounded(&sh.empty[st], (it / stages - 1) & 1, p.timeout_ns, p.err, &sh.abort, true);
+            if (pg < 0 || *static_cast<volatile int*>(&sh.abort)) {
               mbar_arrive(&sh.full[st]);  // no key in this unit
             } else {
               mbar_arrive_expect_tx(&sh.full[st], rec);
@@ -271,7 +251,10 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
     return;
   }
 
-  // -------- consumers: warp w takes the stages w, w + 4, ...
+  // -------- consumers: warp w of the group takes the stages w, w + 4, ...
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+  if (x0 >= x1) return;
+  const int wg = warp % kWarps;
   const int g = lane >> 2, c4 = lane & 3;
   Cursor c = cursor_at<kRows>(p, p.P, x0);
   uint32_t it = 0;
@@ -306,17 +289,15 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
       for (int i = 0; i < LD / 2; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-      // 2^14 <= largest * 2^e < 2^15
-      const int e = min(14 + 127 - static_cast<int>(top >> 7), 120);
-      const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-      sc[half] = p.scale * kLog2e * __ldg(p.g_k + c.h) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+      float up;
+      row_scale(p.scale * __ldg(p.g_k + c.h), top, up, sc[half]);
 #pragma unroll
-      for (int i = 0; i < LD / 2; ++i) {
-        const uint32_t h = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
-        qa[i >> 1][half + 2 * (i & 1)] = h;
-      }
+      for (int i = 0; i < LD / 2; ++i)
+        qa[i >> 1][half + 2 * (i & 1)] =
+            pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xFFFF0000u) * up);
     }
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, nb[2] = {0.0f, 0.0f};
+    uint64_t l2[2] = {0ull, 0ull};
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
     // keys that every row of the tile sees
@@ -327,16 +308,17 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
       all_hi = min(all_hi, __shfl_xor_sync(0xFFFFFFFFu, all_hi, s));
     }
 
-    for (int i = 0; i < n; ++i, ++it) {
-      if ((it & (kWarps - 1)) != static_cast<uint32_t>(warp)) continue;
-      const int st = it % stages;
-      mbar_wait_warp(&sh.full[st], (it / stages) & 1, p.timeout_ns, p.err, &sh.abort);
+    for (int i = (wg - static_cast<int>(it)) & (kWarps - 1); i < n; i += kWarps) {
+      const uint32_t at = it + i;
+      const int st = at % stages;
+      mbar_wait_warp(&sh.full[st], (at / stages) & 1, p.timeout_ns, p.err, &sh.abort);
       const uint8_t* kc = ring + static_cast<size_t>(st) * rec;
       const uint8_t* ks = kc + codes_bytes(p.P, D);
       const uint8_t* vc = kc + rec / 2;
       const uint8_t* vs = vc + codes_bytes(p.P, D);
       const int key0 = (c.u + i) * p.P;
       const int keys = min(p.P, c.s.len - key0);
+#pragma unroll 1
       for (int t0 = 0; t0 < keys; t0 += 32) {
         float s[4][4];
 #pragma unroll
@@ -344,19 +326,16 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
           s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
           const int tok = t0 + 8 * t + (g ^ ((g >> 1) & 1));
           uint32_t w[LD / 8];
+          uint32_t sb[2];
           if (LD == 32) {
             const uint4 v = *reinterpret_cast<const uint4*>(kc + tok * (D / 2) + c4 * 16);
             w[0] = v.x, w[1] = v.y, w[2 % (LD / 8)] = v.z, w[3 % (LD / 8)] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kc + tok * (D / 2) + c4 * 8);
-            w[0] = v.x, w[1] = v.y;
-          }
-          uint32_t sb[2];
-          if (LD == 32) {
             const uint32_t f = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + tok * (D / 16) + 2 * c4));
             sb[0] = __byte_perm(f, f, 0x1010);
             sb[1] = __byte_perm(f, f, 0x3232);
           } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(kc + tok * (D / 2) + c4 * 8);
+            w[0] = v.x, w[1] = v.y;
             const uint32_t f = e4m3x2_to_f16x2(ks[tok * (D / 16) + c4]);
             sb[0] = sb[1] = __byte_perm(f, f, 0x1010);
           }
@@ -372,56 +351,62 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
           }
         }
         const int k0 = key0 + t0;
-        const bool open = k0 >= all_lo && k0 + 32 <= all_hi;  // no key of these is masked for any row
-        float top[2] = {-INFINITY, -INFINITY};
+        if (k0 < all_lo || k0 + 32 > all_hi) {  // some row does not see all of these keys
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int half = q >> 1;
-            float x = s[t][q] * sc[half];
-            if (!open) {
+            for (int q = 0; q < 4; ++q) {
               const int key = k0 + 8 * t + ((2 * c4 + (q & 1)) ^ (c4 & 1));
-              if (key < lo[half] || key >= hi[half]) x = -INFINITY;
+              if (key < lo[q >> 1] || key >= hi[q >> 1]) s[t][q] = -INFINITY;
             }
-            s[t][q] = x;
-            top[half] = fmaxf(top[half], x);
-          }
-        float corr[2];
+        }
+        float top[2];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
-          top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 2));
-          const float mn = fmaxf(m[half], top[half]);
-          const float base = mn == -INFINITY ? 0.0f : mn;
-          corr[half] = ex2(m[half] - base);
-          m[half] = mn;
-          l[half] *= corr[half];
-          top[half] = base - p_shift(kRows);
+          const int q = 2 * half;
+          float a = fmaxf(fmaxf(s[0][q], s[0][q + 1]), s[1][q]);
+          a = fmaxf(fmaxf(a, s[1][q + 1]), s[2][q]);
+          a = fmaxf(fmaxf(a, s[2][q + 1]), s[3][q]);
+          top[half] = fmaxf(a, s[3][q + 1]) * sc[half];
+        }
+        if (__any_sync(0xFFFFFFFFu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+          float f[2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 1));
+            top[half] = fmaxf(top[half], __shfl_xor_sync(0xFFFFFFFFu, top[half], 2));
+            f[half] = 1.0f;
+            if (top[half] > m[half] + kSlack) {
+              f[half] = m[half] == -INFINITY ? 0.0f : ex2(m[half] - top[half]);
+              m[half] = top[half];
+              nb[half] = kShift - top[half];
+            }
+            l2[half] = fma2(l2[half], pair(f[half], f[half]), 0ull);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            o[nt][0] *= f[0], o[nt][1] *= f[0];
+            o[nt][2] *= f[1], o[nt][3] *= f[1];
+          }
         }
         uint32_t pa[2][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float e[4];
+        for (int half = 0; half < 2; ++half) {
+          const uint64_t sc2 = pair(sc[half], sc[half]), nb2 = pair(nb[half], nb[half]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            e[q] = ex2(s[t][q] - top[q >> 1]);
-            l[q >> 1] += e[q];
-          }
-          pa[t >> 1][2 * (t & 1)] = pack_f16x2(e[0], e[1]);
-          pa[t >> 1][2 * (t & 1) + 1] = pack_f16x2(e[2], e[3]);
-        }
-        if (__any_sync(0xFFFFFFFFu, corr[0] != 1.0f || corr[1] != 1.0f)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            o[nt][0] *= corr[0], o[nt][1] *= corr[0];
-            o[nt][2] *= corr[1], o[nt][3] *= corr[1];
+          for (int t = 0; t < 4; ++t) {
+            float a, b;
+            unpair(fma2(pair(s[t][2 * half], s[t][2 * half + 1]), sc2, nb2), a, b);
+            a = ex2(a);
+            b = ex2(b);
+            l2[half] = add2(l2[half], pair(a, b));
+            pa[t >> 1][2 * (t & 1) + half] = pack_f16x2(a, b);
           }
         }
         const bool tail = t0 + 32 > keys;  // some of these keys were never written
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-          uint32_t b[2][NT];
+          uint32_t wa[2][W], wb[2][W], f[2];
 #pragma unroll
           for (int pr = 0; pr < 2; ++pr) {
             const int ta = t0 + 16 * kb + 8 * pr + ((2 * c4) ^ (c4 & 1)), tb = ta ^ 1;
@@ -430,123 +415,134 @@ __global__ void __launch_bounds__(kThreads) attn_rows16_kernel(const AttnParams 
               if (ta >= keys) sa = 0;
               if (tb >= keys) sb = 0;
             }
-            const uint32_t f = e4m3x2_to_f16x2(sa | (sb << 8));
-            constexpr int W = D / 64;  // words of a key per lane
-            uint32_t wa[W], wb[W];
+            f[pr] = e4m3x2_to_f16x2(sa | (sb << 8));
             if (W == 2) {
               const uint2 va = *reinterpret_cast<const uint2*>(vc + ta * (D / 2) + 8 * g);
               const uint2 vb = *reinterpret_cast<const uint2*>(vc + tb * (D / 2) + 8 * g);
-              wa[0] = va.x, wa[W - 1] = va.y, wb[0] = vb.x, wb[W - 1] = vb.y;
+              wa[pr][0] = va.x, wa[pr][W - 1] = va.y, wb[pr][0] = vb.x, wb[pr][W - 1] = vb.y;
             } else {
-              wa[0] = *reinterpret_cast<const uint32_t*>(vc + ta * (D / 2) + 4 * g);
-              wb[0] = *reinterpret_cast<const uint32_t*>(vc + tb * (D / 2) + 4 * g);
-            }
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-              uint32_t even[4], odd[4];
-              e2m1x8((wa[j] & 0x0F0F0F0Fu) | ((wb[j] << 4) & 0xF0F0F0F0u), even);
-              e2m1x8(((wa[j] >> 4) & 0x0F0F0F0Fu) | (wb[j] & 0xF0F0F0F0u), odd);
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                b[pr][8 * j + 2 * q] = hmul2(even[q], f);
-                b[pr][8 * j + 2 * q + 1] = hmul2(odd[q], f);
-              }
+              wa[pr][0] = *reinterpret_cast<const uint32_t*>(vc + ta * (D / 2) + 4 * g);
+              wb[pr][0] = *reinterpret_cast<const uint32_t*>(vc + tb * (D / 2) + 4 * g);
             }
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt], pa[kb], b[0][nt], b[1][nt]);
+          for (int j = 0; j < W; ++j)
+#pragma unroll
+            for (int odd = 0; odd < 2; ++odd) {
+              uint32_t b[2][4];
+#pragma unroll
+              for (int pr = 0; pr < 2; ++pr) {
+                e2m1x8(odd ? ((wa[pr][j] >> 4) & 0x0F0F0F0Fu) | (wb[pr][j] & 0xF0F0F0F0u)
+                           : (wa[pr][j] & 0x0F0F0F0Fu) | ((wb[pr][j] << 4) & 0xF0F0F0F0u),
+                       b[pr]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) b[pr][q] = hmul2(b[pr][q], f[pr]);
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) mma_f16(o[8 * j + 2 * q + odd], pa[kb], b[0][q], b[1][q]);
+            }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.empty[st]);
     }
+    it += n;
 
-    // -------- the four warps' results become one
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 1);
-      l[half] += __shfl_xor_sync(0xFFFFFFFFu, l[half], 2);
-      if (c4 == 0) {
-        sh.m[warp][g + 8 * half] = m[half];
-        sh.l[warp][g + 8 * half] = l[half];
-      }
-      // lane's LD consecutive columns, 16-byte chunks moved so that the eight
-      // lanes of a store phase hit different banks
-      const int r = g + 8 * half;
-#pragma unroll
-      for (int v = 0; v < LD / 4; ++v) {
-        float4 f;
-        float* fp = reinterpret_cast<float*>(&f);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int col = 4 * v + q;  // of the lane's LD: column tile col % NT, second column of the pair from NT on
-          fp[q] = o[col % NT][2 * half + col / NT];
-        }
-        const int chunk = (LD / 4) * c4 + v;
-        *reinterpret_cast<float4*>(&sh.o[warp][r][4 * (chunk ^ ((c4 + 4 * (r & 1)) & (D / 4 - 1)))]) = f;
-      }
-    }
-    named_bar_sync(1, 32 * kWarps);
+    // -------- the four warps' results become one, half the columns at a time
     const bool whole = c.u == c.u0 && n == c.u1 - c.u0;
     const int rows = min(kRows, c.s.n * p.G - c.tile * kRows);
-    const long long slot = 2ll * blockIdx.x + (c.u == c.u0 ? 1 : 0);
-    constexpr int CH = D / 4;  // 16-byte chunks of a row
-    for (int k = threadIdx.x; k < rows * CH; k += 32 * kWarps) {
-      const int r = k / CH, q = k % CH;
-      float mm = -INFINITY;
+    const long long slot = 2ll * block + (c.u == c.u0 ? 1 : 0);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][r]);
-      const float base = mm == -INFINITY ? 0.0f : mm;
-      float ll = 0.0f;
-      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      const int at = 4 * (q ^ ((q / (LD / 4) + 4 * (r & 1)) & (D / 4 - 1)));
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2f(sh.m[w][r] - base);
-        const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][r][at]);
-        ll += f * sh.l[w][r];
-        a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
+    for (int half = 0; half < 2; ++half) {
+      float l, lb;
+      unpair(l2[half], l, lb);
+      l += lb;
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+      l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+      if (c4 == 0) {
+        sh.m[wg][g + 8 * half] = m[half];
+        sh.l[wg][g + 8 * half] = l;
       }
-      if (whole) {
-        const int idx = c.tile * kRows + r;
-        const long long row = static_cast<long long>(c.s.q0 + idx / p.G) * p.Hq + c.h * p.G + idx % p.G;
-        const float inv = ll > 0.0f ? __ldg(p.g_v + c.h) / ll : 0.0f;
-        *reinterpret_cast<uint2*>(p.out + row * D + 4 * q) =
-            make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        if (p.lse && q == 0) p.lse[row] = ll > 0.0f ? (mm + log2f(ll) - p_shift(kRows)) * (1.0f / kLog2e) : -INFINITY;
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D + 4 * q) = a;
-        if (q == 0) {
-          p.part_ml[slot * 2 * kRows + r] = mm;
-          p.part_ml[(slot * 2 + 1) * kRows + r] = ll;
+    }
+    // Lane's columns of a row are LD * c4 .. + LD; part k of two holds the
+    // lane's columns [k * LD / 2, (k + 1) * LD / 2).  16-byte chunks are moved so
+    // that the eight lanes of a store phase hit different banks.
+#pragma unroll
+    for (int part = 0; part < 2; ++part) {
+      if (part) named_bar_sync(1 + grp, 32 * kWarps);  // the first half has been read
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = g + 8 * half;
+#pragma unroll
+        for (int v = 0; v < LD / 8; ++v) {
+          float4 f;
+          float* fp = reinterpret_cast<float*>(&f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) fp[q] = o[4 * v + q][2 * half + part];  // LD / 2 = NT columns: tile 4v + q
+          const int chunk = (LD / 8) * c4 + v;
+          *reinterpret_cast<float4*>(&sh.o[wg][r][4 * (chunk ^ ((c4 + 4 * (r & 1)) & (D / 8 - 1)))]) = f;
+        }
+      }
+      named_bar_sync(1 + grp, 32 * kWarps);
+      constexpr int CH = D / 8;  // 16-byte chunks of half a row
+      for (int k = wg * 32 + lane; k < rows * CH; k += 32 * kWarps) {
+        const int r = k / CH, q = k % CH;
+        const int col = (q / (LD / 8)) * LD + part * (LD / 2) + 4 * (q % (LD / 8));
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, sh.m[w][r]);
+        const float base = mm == -INFINITY ? 0.0f : mm;
+        float ll = 0.0f;
+        float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const int from = 4 * (q ^ ((q / (LD / 8) + 4 * (r & 1)) & (D / 8 - 1)));
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(sh.m[w][r] - base);
+          const float4 v = *reinterpret_cast<const float4*>(&sh.o[w][r][from]);
+          ll += f * sh.l[w][r];
+          a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
+        }
+        if (whole) {
+          const int idx = c.tile * kRows + r;
+          const long long row = static_cast<long long>(c.s.q0 + idx / p.G) * p.Hq + c.h * p.G + idx % p.G;
+          const float inv = ll > 0.0f ? __ldg(p.g_v + c.h) / ll : 0.0f;
+          *reinterpret_cast<uint2*>(p.out + row * D + col) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          if (p.lse && q == 0 && part == 0)
+            p.lse[row] = ll > 0.0f ? (mm + log2f(ll) - kShift) * (1.0f / kLog2e) : -INFINITY;
+        } else {
+          *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D + col) = a;
+          if (q == 0 && part == 0) {
+            p.part_ml[slot * 2 * kRows + r] = mm;
+            p.part_ml[(slot * 2 + 1) * kRows + r] = ll;
+          }
         }
       }
     }
-    named_bar_sync(1, 32 * kWarps);
+    named_bar_sync(1 + grp, 32 * kWarps);
     left -= n;
     if (left > 0) cursor_next<kRows>(p, p.P, c);
   }
 }
 
-constexpr int kRingBytes = 72 * 1024;
-
 template <int D>
 int launch_rows16(const AttnParams& p, cudaStream_t s) {
   const int rec = record_bytes(p.P, D);
-  const int stages = std::min(kMaxStages, std::max(4, kRingBytes / rec));
-  const int smem = static_cast<int>(round_up(sizeof(Shared<D>), 128)) + stages * rec;
-  static int set[64] = {0};
+  const int head = static_cast<int>(round_up(sizeof(Group<D>), 128));
+  const int stages = std::min(kMaxStages, (kSmem / kGroups - head) / rec);
+  const int smem = kGroups * (head + stages * rec);
+  static bool set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  if (set[dev] < smem) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_rows16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (!set[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(attn_rows16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) {
       set_cuda_error(e);
       return MOE_ERR_CUDA;
     }
-    set[dev] = smem;
+    set[dev] = true;
   }
-  attn_rows16_kernel<D><<<p.blocks, kThreads, smem, s>>>(p, stages);
+  attn_rows16_kernel<D><<<p.blocks / kGroups, kThreads, smem, s>>>(p, stages);
   return check_launch();
 }
 
@@ -576,7 +572,7 @@ Layout layout(AttnParams& p, int D, void* ws) {
   // Up to 32 rows per sequence and kv head on average: 16 rows at a time.
   const bool tiles16 = static_cast<long long>(p.T) * p.G <= 32ll * p.B;
   r.rows = tiles16 ? kRows : kTileRows;
-  r.blocks = tiles16 ? 2 * num_sms() : num_sms();
+  r.blocks = tiles16 ? kGroups * num_sms() : num_sms();
   Carve c(ws, 0);
   const long long tiles = static_cast<long long>(p.T) * p.G / r.rows + p.B + 1;
   p.starts = c.take<int>(p.B + 1);

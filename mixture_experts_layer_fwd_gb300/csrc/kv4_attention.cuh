@@ -6,7 +6,7 @@
 // head read its keys and values once.  An item's work is counted in units of
 // keys (pages, or tiles of 128 keys).  All units of all items, in the order
 // (sequence, kv head, row tile), are one line that is cut into equal ranges,
-// one per block: every block has the same work whatever the lengths are, and
+// one per block (or group of its warps): every block has the same work whatever the lengths are, and
 // at most two items per block are left incomplete, one at each end of its
 // range.  Those go to the workspace as (sum, maximum, unnormalised output)
 // and are joined, in the order of the blocks, by a second kernel.
@@ -17,14 +17,72 @@
 namespace moe {
 namespace kv4 {
 
-// P is held as p * 2^shift in fp16, p the weight relative to the running
-// maximum: normal numbers reach down to 2^(-14-shift), and what is lost below
-// is at most 2^(-25-shift) per key.  The largest value is 2^15: the 16-row
-// kernel's maximum is exact, the 256-row kernel's lags by up to 2^8.  The sums
-// and O carry the factor too, so it cancels except in the log of the sum.
+// P is held as p * 2^kShift in fp16, p the weight relative to the running
+// maximum.  That maximum is moved only when a row's grows by more than
+// 2^kSlack, so O is hardly ever rescaled; P reaches 2^15 at most, its normal
+// numbers reach down to 2^(-14 - kShift), and what is lost below is at most
+// 2^(-25 - kShift) per key.  The sums and O carry the factor too, so it cancels
+// except in the log of the sum.
 constexpr int kRowsSmall = 16, kRowsTile = 256;
-constexpr float kSlack = 8.0f;
-__host__ __device__ constexpr float p_shift(int rows) { return rows == kRowsSmall ? 15.0f : 15.0f - kSlack; }
+constexpr float kSlack = 8.0f, kShift = 15.0f - kSlack;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 2^x by the hardware's approximation (2 ulp), 0 for -infinity
+DEVINL float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+DEVINL uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Four bytes of E2M1 pairs -> four fp16 pairs (low nibble first).
+DEVINL void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+// Pairs of fp32 in one register pair.
+DEVINL uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+DEVINL void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A query row's power of two and softmax scale, from its largest magnitude (as
+// bf16 bits): |q| * up stays below 2^15, and scores in log2 units are sc times
+// the products.  sc > 0: the sign of the scale goes into up, a zero scale
+// into a zero row, so that the largest score is that of the largest product.
+DEVINL void row_scale(float scale_gk, uint32_t top, float& up, float& sc) {
+  const int e = min(14 + 127 - static_cast<int>(top >> 7), 120);
+  up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  sc = scale_gk * kLog2e * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  if (sc < 0.0f) sc = -sc, up = -up;
+  if (sc == 0.0f) sc = 1.0f, up = 0.0f;
+}
 
 struct AttnParams {
   const uint16_t* q;  // bf16 [T][Hq][D], q_stride elements between tokens
@@ -40,7 +98,7 @@ struct AttnParams {
   int* starts;          // [B + 1] q_offsets as used: inside [0, T], never falling
   int* tile_base;       // [B + 1] row tiles before sequence b
   long long* unit_sum;  // [tiles + 1] units of one kv head before row tile f
-  int blocks;           // blocks of the main kernel
+  int blocks;           // ranges: blocks of the main kernel, or groups of its warps
   int min_units;        // least units of a block's range
   // partial results: slot 2 * block (the item begun by an earlier block) and 2 * block + 1
   float *part_o, *part_ml;  // [2 * blocks][ROWS][D], [2 * blocks][2][ROWS]

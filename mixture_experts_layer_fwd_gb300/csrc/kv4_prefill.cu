@@ -32,7 +32,6 @@ constexpr int kRows = kRowsTile;
 constexpr int kKeys = 128;
 constexpr int kThreads = 512;
 constexpr int kMaxSlots = 16;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kExpand0 = 8, kLoad = 12, kMma = 13, kWait = 14;
 
 template <int D>
@@ -62,47 +61,6 @@ DEVINL void umma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, ui
       "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
-}
-DEVINL float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-DEVINL uint32_t pack_f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-DEVINL uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-DEVINL void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-DEVINL uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-DEVINL void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
-      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-DEVINL uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -153,11 +111,8 @@ DEVINL float load_q(const AttnParams& p, const Cursor& c, int idx, int r, uint32
       for (int q = 0; q < 4; ++q) top = max(top, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
     }
   }
-  const int e = min(14 + 127 - static_cast<int>(top >> 7), 120);  // 2^14 <= largest * 2^e < 2^15
-  float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  float sc = p.scale * kLog2e * __ldg(p.g_k + c.h) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-  if (sc < 0.0f) sc = -sc, up = -up;  // the maximum of S has to be that of the scores
-  if (sc == 0.0f) sc = 1.0f, up = 0.0f;
+  float up, sc;
+  row_scale(p.scale * __ldg(p.g_k + c.h), top, up, sc);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
     uint4 v = make_uint4(0, 0, 0, 0);
@@ -279,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               if (grow) {
                 f = m == -INFINITY ? 0.0f : ex2(m - top);
                 m = top;
-                nb = p_shift(kRows) - top;
+                nb = kShift - top;
               }
               const uint64_t ff = pair(f, f);
 #pragma unroll
@@ -354,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 }
               }
             }
-            if (p.lse && have) p.lse[row] = l > 0.0f ? (m + log2f(l) - p_shift(kRows)) * (1.0f / kLog2e) : -INFINITY;
+            if (p.lse && have) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
           } else {
             const long long slot = 2ll * blockIdx.x + (c.u == c.u0 ? 1 : 0);
             const int rr = g * 128 + r;
