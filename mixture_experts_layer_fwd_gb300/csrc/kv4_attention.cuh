@@ -215,6 +215,87 @@ DEVINL void cursor_next(const AttnParams& p, int unit, Cursor& c) {
   cursor_item<ROWS>(p, unit, c);
 }
 
+// What the roles of a block need of an item: one warp walks the line of units
+// and publishes them, so that the divisions and searches are in the program
+// once and the loops over keys stay in the instruction cache.
+struct Item {
+  int row0;    // first of its rows (token, head of the kv head) in the sequence
+  int rows;    // rows that are there
+  int q0, nq, len;  // first query row of the sequence, its queries, its keys
+  int b, h;
+  int u, n;    // first unit here, and how many (0: no more items)
+  int slot;    // -1: the whole item is here; else where its partial result goes
+};
+constexpr int kItems = 8;
+struct ItemRing {
+  Item item[kItems];
+  uint64_t full[kItems], empty[kItems];
+};
+DEVINL void item_ring_init(ItemRing& r, int readers) {
+  for (int i = 0; i < kItems; ++i) {
+    mbar_init(&r.full[i], 1);
+    mbar_init(&r.empty[i], readers);
+  }
+}
+template <int ROWS>
+DEVINL Item make_item(const AttnParams& p, const Cursor& c, int n, int block) {
+  Item t;
+  t.row0 = c.tile * ROWS;
+  t.rows = min(ROWS, c.s.n * p.G - t.row0);
+  t.q0 = c.s.q0, t.nq = c.s.n, t.len = c.s.len;
+  t.b = c.b, t.h = c.h, t.u = c.u, t.n = n;
+  t.slot = c.u == c.u0 ? (n == c.u1 - c.u0 ? -1 : 2 * block + 1) : 2 * block;
+  return t;
+}
+// Keys of row idx of an item's sequence.
+DEVINL void item_keys(const AttnParams& p, const Item& t, int idx, int& lo, int& hi) {
+  const Seq s{t.q0, t.nq, t.len};
+  row_keys(p, s, idx / p.G, lo, hi);
+}
+
+// Bounded wait of a whole warp, every lane testing: mbar_wait_bounded's rules.
+DEVINL void wait_warp(uint64_t* bar, uint32_t parity, unsigned long long tmo, unsigned int* err, volatile int* abort) {
+  uint64_t t0 = 0;
+  while (!mbar_try_wait_suspend(bar, parity, 20000u)) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort || now - t0 > tmo) {
+      atomicOr(err, kErrTimeout);
+      *abort = 1;
+      break;
+    }
+  }
+  __syncwarp();
+}
+// One reader's (a warp's) place in an ItemRing.
+struct ItemReader {
+  int i = 0;
+  DEVINL Item next(ItemRing& r, unsigned long long tmo, unsigned int* err, volatile int* abort) {
+    const int k = i & (kItems - 1);
+    wait_warp(&r.full[k], (i / kItems) & 1, tmo, err, abort);
+    Item t = r.item[k];
+    if (*abort) t.n = 0;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[k]);
+    ++i;
+    return t;
+  }
+};
+// The publishing warp's side (the item is the same in every lane).
+struct ItemWriter {
+  int i = 0;
+  DEVINL void put(ItemRing& r, const Item& t, unsigned long long tmo, unsigned int* err, volatile int* abort) {
+    const int k = i & (kItems - 1);
+    if (i >= kItems) wait_warp(&r.empty[k], (i / kItems - 1) & 1, tmo, err, abort);
+    if ((threadIdx.x & 31) == 0) {
+      r.item[k] = t;
+      mbar_arrive(&r.full[k]);
+    }
+    __syncwarp();
+    ++i;
+  }
+};
+
 DEVINL long long total_units(const AttnParams& p) { return p.unit_sum[p.tile_base[p.B]] * p.Hkv; }
 DEVINL long long range_of(const AttnParams& p, long long total) {
   const long long r = (total + p.blocks - 1) / p.blocks;

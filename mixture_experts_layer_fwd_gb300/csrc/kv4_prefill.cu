@@ -12,6 +12,7 @@
 //   12        bulk copies of the halves (keys, values) of page records
 //   13        issues the matrix instructions, 14 waits for it (a wait in the
 //             issuing warp would queue behind its instructions)
+//   15        walks the block's items and publishes them to the others
 //
 // S = Q K^T comes from shared memory, O += P V takes P from tensor memory.  The
 // order of issue is P_A V, Q_A K', P_B V, Q_B K' (K' the next tile), so that
@@ -32,7 +33,8 @@ constexpr int kRows = kRowsTile;
 constexpr int kKeys = 128;
 constexpr int kThreads = 512;
 constexpr int kMaxSlots = 16;
-constexpr int kExpand0 = 8, kLoad = 12, kMma = 13, kWait = 14;
+constexpr int kExpand0 = 8, kLoad = 12, kMma = 13, kWalk = 15;  // 14 waits for 13
+constexpr int kReaders = 8 + 4 + 3;
 
 template <int D>
 struct Cfg {
@@ -48,6 +50,7 @@ struct Bars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t qfull[2], sfull[2], pfull[2], ofull[2], done;
+  ItemRing items;
   uint32_t tmem;
   int abort;
 };
@@ -63,47 +66,20 @@ DEVINL void umma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, ui
       : "memory");
 }
 DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+  // no memory clobber: loads of record bytes may move past stores to operand tiles
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
-// The block's tiles of keys, in order.
-struct Tiles {
-  Cursor c;
-  long long left;  // tiles of this block's range from the current one on
-  int n;           // tiles of the current item from the current one on
-  bool two;        // the item has rows in tile B
-  bool first;      // the current tile is the item's first here
-  DEVINL void item(const AttnParams& p) {
-    n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
-    two = c.s.n * static_cast<long long>(p.G) - static_cast<long long>(c.tile) * kRows > 128;
-    first = true;
-  }
-  DEVINL Tiles(const AttnParams& p, long long x0, long long x1) : c(cursor_at<kRows>(p, kKeys, x0)), left(x1 - x0) {
-    item(p);
-  }
-  DEVINL void next(const AttnParams& p) {
-    --left;
-    if (left <= 0) return;
-    if (--n == 0) {
-      cursor_next<kRows>(p, kKeys, c);
-      item(p);
-    } else {
-      ++c.u;
-      first = false;
-    }
-  }
-};
-
 // One query row (thread's) to fp16 in the swizzled tile; returns the softmax
-// scale of the row in log2 units (>= 0).
+// scale of the row in log2 units (> 0).
 template <int D>
-DEVINL float load_q(const AttnParams& p, const Cursor& c, int idx, int r, uint32_t tile) {
-  const bool have = idx < c.s.n * p.G;
+DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, uint32_t tile) {
+  const bool have = idx < t.nq * p.G;
   const int tok = idx / p.G;
-  const uint4* src = reinterpret_cast<const uint4*>(p.q + (c.s.q0 + tok) * p.q_stride + (c.h * p.G + idx % p.G) * D);
+  const uint4* src = reinterpret_cast<const uint4*>(p.q + (t.q0 + tok) * p.q_stride + (t.h * p.G + idx - tok * p.G) * D);
   uint32_t top = 0;
   if (have) {
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < D / 8; ++i) {
       const uint4 v = __ldg(src + i);
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -112,8 +88,8 @@ DEVINL float load_q(const AttnParams& p, const Cursor& c, int idx, int r, uint32
     }
   }
   float up, sc;
-  row_scale(p.scale * __ldg(p.g_k + c.h), top, up, sc);
-#pragma unroll
+  row_scale(p.scale * __ldg(p.g_k + t.h), top, up, sc);
+#pragma unroll 2
   for (int i = 0; i < D / 8; ++i) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (have) v = __ldg(src + i);
@@ -156,6 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       mbar_init(&bars.ofull[i], 1);
     }
     mbar_init(&bars.done, 1);
+    item_ring_init(bars.items, kReaders);
     bars.abort = 0;
     fence_mbar_init();
   }
@@ -170,6 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
 
   const long long total = total_units(p), range = range_of(p, total);
   const long long x0 = blockIdx.x * range, x1 = min(total, x0 + range);
+  int* const abort = &bars.abort;
   if (x0 < x1) {
     if (warp < 8) {
       // ================================================================ softmax
@@ -180,43 +158,92 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       const uint32_t ts = tmem + lanes + g * 128, to = tmem + lanes + 256 + g * 128;
       const uint32_t tile_q = sq + g * C::Q_BYTES;
       uint32_t cnt = 0;  // tiles of keys done
-      bool loaded = false;
+      ItemReader items;
+      Item it, nx = items.next(bars.items, tmo, p.err, abort);
+      bool done_one = false;          // `it` holds an item whose output is still in tensor memory
       float sc = 0.0f;
-      Cursor c = cursor_at<kRows>(p, kKeys, x0);
-      long long left = x1 - x0;
-      while (left > 0) {
-        const int n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
-        const int row0 = c.tile * kRows;
-        const bool mine = g == 0 || c.s.n * p.G - row0 > 128;
+      float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units); P's shift less it (0 for none)
+      uint64_t l2[2] = {0ull, 0ull};
+      while (true) {
+        // the next item's queries while the last products of this one run
+        const bool mine = nx.n > 0 && nx.rows > g * 128;
+        float sc_next = 0.0f;
         if (mine) {
-          const int idx = row0 + g * 128 + r;
-          if (!loaded) {
-            sc = load_q<D>(p, c, idx, r, tile_q);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.qfull[g]);
+          sc_next = load_q<D>(p, nx, nx.row0 + g * 128 + r, r, tile_q);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.qfull[g]);
+        }
+        if (done_one) {
+          const int rr = g * 128 + r, idx = it.row0 + rr;
+          wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
+          tc_fence_after();
+          float l, lb;
+          unpair(add2(l2[0], l2[1]), l, lb);
+          l += lb;
+          const int tok = idx / p.G;
+          const long long row = static_cast<long long>(it.q0 + tok) * p.Hq + it.h * p.G + (idx - tok * p.G);
+          const bool whole = it.slot < 0, have = rr < it.rows;
+          const float inv = l > 0.0f ? __ldg(p.g_v + it.h) / l : 0.0f;
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(to + 32 * q, o);
+            tmem_ld_wait();
+            if (whole) {
+              if (have) {
+                uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + 32 * q);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    w[k] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * k]) * inv, __uint_as_float(o[8 * v + 2 * k + 1]) * inv);
+                  dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              }
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (static_cast<long long>(it.slot) * kRows + rr) * D + 32 * q);
+#pragma unroll
+              for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            }
           }
-          loaded = false;
-          int lo = 0, hi = c.s.len;  // a row that is not there masks nothing
-          const bool have = idx < c.s.n * p.G;
-          if (have) row_keys(p, c.s, idx / p.G, lo, hi);
-          float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units); P's shift less it (0 for none)
-          uint64_t l2[2] = {0ull, 0ull};
-          for (int i = 0; i < n; ++i, ++cnt) {
-            mbar_wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, &bars.abort);
+          if (!whole) {
+            p.part_ml[static_cast<long long>(it.slot) * 2 * kRows + rr] = m;
+            p.part_ml[(static_cast<long long>(it.slot) * 2 + 1) * kRows + rr] = l;
+          } else if (p.lse && have) {
+            p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+          }
+          tc_fence_before();
+        }
+        if (nx.n == 0) break;
+        it = nx;
+        done_one = mine;
+        if (mine) {
+          sc = sc_next;
+          const int idx = it.row0 + g * 128 + r;
+          int lo = 0, hi = it.len;  // a row that is not there masks nothing
+          if (g * 128 + r < it.rows) item_keys(p, it, idx, lo, hi);
+          m = -INFINITY, nb = 0.0f;
+          l2[0] = l2[1] = 0ull;
+          for (int i = 0; i < it.n; ++i, ++cnt) {
+            wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, abort);
             tc_fence_after();
             uint32_t s[4][32];
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(ts + 32 * q, s[q]);
             tmem_ld_wait();
-            const int k0 = (c.u + i) * kKeys;
-            if (!__all_sync(0xFFFFFFFFu, lo <= k0 && k0 + kKeys <= hi)) {
-              const int a = lo - k0, b = hi - k0;
+            const int a = lo - (it.u + i) * kKeys, b = hi - (it.u + i) * kKeys;  // the row's keys, in the tile
+            if (!__all_sync(0xFFFFFFFFu, a <= 0 && b >= kKeys)) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q)
+              for (int q = 0; q < 4; ++q) {
+                // bit j: key 32 q + j is seen
+                const int x = min(max(a - 32 * q, 0), 32), y = min(max(b - 32 * q, 0), 32);
+                const uint32_t see = static_cast<uint32_t>(((1ull << y) - 1ull) & ~((1ull << x) - 1ull));
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (32 * q + j < a || 32 * q + j >= b) s[q][j] = 0xFF800000u;  // -infinity
+                  if (!(see & (1u << j))) s[q][j] = 0xFF800000u;  // -infinity
+              }
             }
             float mx[4];
 #pragma unroll
@@ -240,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
 #pragma unroll
               for (int q = 0; q < 2; ++q) l2[q] = fma2(l2[q], ff, 0ull);
               if (i > 0) {  // O holds something: bring it to the new maximum
-                mbar_wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, &bars.abort);
+                wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
@@ -259,12 +286,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               uint32_t w[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
-                float a, b;
-                unpair(fma2(pair(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), sc2, nb2), a, b);
-                a = ex2(a);
-                b = ex2(b);
-                l2[j & 1] = add2(l2[j & 1], pair(a, b));
-                w[j] = pack_f16x2(a, b);
+                float x, y;
+                unpair(fma2(pair(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), sc2, nb2), x, y);
+                x = ex2(x);
+                y = ex2(y);
+                l2[j & 1] = add2(l2[j & 1], pair(x, y));
+                w[j] = pack_f16x2(x, y);
               }
               tmem_st_32x32b_x16(ts + 16 * q, w);
             }
@@ -273,62 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.pfull[g]);
           }
-          // the next item's queries while the last products run
-          Cursor nx = c;
-          if (left > n) cursor_next<kRows>(p, kKeys, nx);
-          if (left > n && (g == 0 || nx.s.n * p.G - nx.tile * kRows > 128)) {
-            sc = load_q<D>(p, nx, nx.tile * kRows + g * 128 + r, r, tile_q);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.qfull[g]);
-            loaded = true;
-          }
-          mbar_wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, &bars.abort);
-          tc_fence_after();
-          float l, la, lb;
-          unpair(add2(l2[0], l2[1]), la, lb);
-          l = la + lb;
-          const bool whole = c.u == c.u0 && n == c.u1 - c.u0;
-          if (whole) {
-            const long long row = static_cast<long long>(c.s.q0 + idx / p.G) * p.Hq + c.h * p.G + idx % p.G;
-            const float inv = l > 0.0f ? __ldg(p.g_v + c.h) / l : 0.0f;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + 32 * q, o);
-              tmem_ld_wait();
-              if (have) {
-                uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + 32 * q);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                  uint32_t w[4];
-#pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    w[k] = pack_bf16x2(__uint_as_float(o[8 * v + 2 * k]) * inv, __uint_as_float(o[8 * v + 2 * k + 1]) * inv);
-                  dst[v] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              }
-            }
-            if (p.lse && have) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
-          } else {
-            const long long slot = 2ll * blockIdx.x + (c.u == c.u0 ? 1 : 0);
-            const int rr = g * 128 + r;
-#pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(to + 32 * q, o);
-              tmem_ld_wait();
-              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (slot * kRows + rr) * D + 32 * q);
-#pragma unroll
-              for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-            }
-            p.part_ml[slot * 2 * kRows + rr] = m;
-            p.part_ml[(slot * 2 + 1) * kRows + rr] = l;
-          }
-          tc_fence_before();
         }
-        left -= n;
-        if (left > 0) cursor_next<kRows>(p, kKeys, c);
+        nx = items.next(bars.items, tmo, p.err, abort);
       }
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -338,204 +311,256 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         const int tg = lane & 7, tgh = w & 1;  // V: group of 8 keys in a 64-key sub-tile
         const int blk = D == 128 ? (2 * (tg >> 1) + (lane >> 3) + 4 * (w >> 1)) & 7 : (2 * (tg >> 1) + (lane >> 3)) & 3;
         const int odd = tg & 1;
-        Tiles t(p, x0, x1);
-        uint32_t s = 0;  // halves taken from the ring
-        for (uint32_t j = 0; t.left > 0; ++j, t.next(p)) {
-          const uint32_t st = j & 1, ph = (j >> 1) & 1;
-          // ---- K
-          if (j >= 2) mbar_wait_warp(&bars.kempty[st], ph ^ 1, tmo, p.err, &bars.abort);
-          const uint32_t kt = sk + st * C::K_BYTES;
-          for (int pg = 0; pg < pages; ++pg, ++s) {
-            const uint32_t slot = s % slots;
-            mbar_wait_warp(&bars.full[slot], (s / slots) & 1, tmo, p.err, &bars.abort);
-            const uint8_t* kc = ring + slot * half;
-            const uint8_t* ks = kc + codes_bytes(p.P, D);
-            for (int t0 = 8 * w; t0 < p.P; t0 += 32) {
-              const int in = t0 + (lane >> 2), key = pg * p.P + in;
+        const int logp = p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
+        int slot = 0;        // of the ring's next half
+        uint32_t round = 0;  // its parity
+        // Byte offset of a key's half, the key counted in the tile.
+        auto half_of = [&](int key) {
+          int sl = slot + (key >> logp);
+          if (sl >= slots) sl -= slots;
+          return sl * half;
+        };
+        ItemReader items;
+        uint32_t j = 0;
+        while (true) {
+          const Item it = items.next(bars.items, tmo, p.err, abort);
+          if (it.n == 0) break;
+          for (int i = 0; i < 2 * it.n; ++i) {  // K, V, K, V, ...
+            const bool is_v = i & 1;
+            const uint32_t st = j & 1, ph = (j >> 1) & 1;
+            {
+              int sl = slot;
+              uint32_t rd = round;
+              for (int pg = 0; pg < pages; ++pg) {
+                wait_warp(&bars.full[sl], rd, tmo, p.err, abort);
+                if (++sl == slots) sl = 0, rd ^= 1;
+              }
+            }
+            if (j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, tmo, p.err, abort);
+            if (!is_v) {
+              // lane = (key, quarter of its values); the warp's keys are 32k + 8w ..
               constexpr int W = D / 32;  // words of 8 codes per lane
-              uint32_t cw[W];
-              uint32_t sb[2];
-              if (W == 4) {
-                const uint4 v = *reinterpret_cast<const uint4*>(kc + in * (D / 2) + 16 * c4);
-                // lanes 2, 3 of a key write their chunks in another order: no two of a phase on the same banks
-                const bool hi = c4 & 2;
-                cw[0] = hi ? v.z : v.x, cw[1] = hi ? v.w : v.y, cw[2 % W] = hi ? v.x : v.z, cw[3 % W] = hi ? v.y : v.w;
-                const uint32_t f = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + in * (D / 16) + 2 * c4));
-                sb[0] = __byte_perm(f, f, hi ? 0x3232 : 0x1010);
-                sb[1] = __byte_perm(f, f, hi ? 0x1010 : 0x3232);
-              } else {
-                const uint2 v = *reinterpret_cast<const uint2*>(kc + in * (D / 2) + 8 * c4);
-                cw[0] = v.x, cw[1] = v.y;
-                const uint32_t f = e4m3x2_to_f16x2(ks[in * (D / 16) + c4]);
-                sb[0] = sb[1] = __byte_perm(f, f, 0x1010);
-              }
-              const uint32_t row = kt + (W == 4 ? (c4 >> 1) * C::SUB_Q : 0) + key * 128;
+              uint32_t cw[4][W], sb[4];
+              const bool hi = W == 4 && (c4 & 2);
+              const int key0 = 8 * w + (lane >> 2);
 #pragma unroll
-              for (int i = 0; i < W; ++i) {
-                uint32_t h[4];
-                e2m1x8(cw[i], h);
-                const int chunk = W == 4 ? 4 * (c4 & 1) + (i ^ (c4 & 2)) : 2 * c4 + i;
-                const uint32_t f = sb[W == 4 ? i >> 1 : 0];
-                st_shared_v4(row + ((chunk ^ (key & 7)) << 4), hmul2(h[0], f), hmul2(h[1], f), hmul2(h[2], f),
-                             hmul2(h[3], f));
-              }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.empty[slot]);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.kfull[st]);
-          // ---- V
-          if (j >= 2) mbar_wait_warp(&bars.vempty[st], ph ^ 1, tmo, p.err, &bars.abort);
-          for (int pg = 0; pg < pages; ++pg)
-            mbar_wait_warp(&bars.full[(s + pg) % slots], ((s + pg) / slots) & 1, tmo, p.err, &bars.abort);
-          if (D == 128 || w < 2) {
-            const int first = tgh * 64 + tg * 8;  // the thread's 8 keys in the tile
-            const uint8_t* vc = ring + ((s + first / p.P) % slots) * half + (first % p.P) * (D / 2) + 8 * blk;
-            const uint8_t* vs = ring + ((s + first / p.P) % slots) * half + codes_bytes(p.P, D) +
-                                (first % p.P) * (D / 16) + blk;
-            const int keys = t.c.s.len - t.c.u * kKeys - first;  // of the 8 that were written
-            uint2 cw[8];
-            uint32_t sb[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {  // register i: key i ^ odd, so that neighbours read different banks
-              cw[i] = *reinterpret_cast<const uint2*>(vc + (i ^ odd) * (D / 2));
-              sb[i] = (i ^ odd) < keys ? vs[(i ^ odd) * (D / 16)] : 0u;
-            }
-            uint32_t f[4];
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              const uint32_t a = odd ? sb[2 * m + 1] : sb[2 * m], b = odd ? sb[2 * m] : sb[2 * m + 1];
-              f[m] = e4m3x2_to_f16x2(a | (b << 8));
-            }
-            const uint32_t vt = sv + st * C::K_BYTES + tgh * C::SUB_V + 16 * blk * 128;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              uint32_t h[8][4];
-#pragma unroll
-              for (int m = 0; m < 4; ++m) {
-                const uint32_t x = v ? cw[2 * m].y : cw[2 * m].x, y = v ? cw[2 * m + 1].y : cw[2 * m + 1].x;
-                const uint32_t a = odd ? y : x, b = odd ? x : y;
-                uint32_t even[4], odds[4];
-                e2m1x8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even);
-                e2m1x8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odds);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  h[2 * q][m] = hmul2(even[q], f[m]);
-                  h[2 * q + 1][m] = hmul2(odds[q], f[m]);
+              for (int k = 0; k < 4; ++k) {
+                const int in = (32 * k + key0) & (p.P - 1);
+                const uint8_t* kc = ring + half_of(32 * k);
+                if (W == 4) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(kc + in * (D / 2) + 16 * c4);
+                  cw[k][0] = v.x, cw[k][1] = v.y, cw[k][2 % W] = v.z, cw[k][3 % W] = v.w;
+                  sb[k] = *reinterpret_cast<const uint16_t*>(kc + codes_bytes(p.P, D) + in * (D / 16) + 2 * c4);
+                } else {
+                  const uint2 v = *reinterpret_cast<const uint2*>(kc + in * (D / 2) + 8 * c4);
+                  cw[k][0] = v.x, cw[k][1] = v.y;
+                  sb[k] = kc[codes_bytes(p.P, D) + in * (D / 16) + c4];
                 }
               }
+              const uint32_t row = sk + st * C::K_BYTES + (W == 4 ? (c4 >> 1) * C::SUB_Q : 0) + key0 * 128;
 #pragma unroll
-              for (int k = 0; k < 8; ++k)
-                st_shared_v4(vt + (8 * v + k) * 128 + ((tg ^ k) << 4), h[k][0], h[k][1], h[k][2], h[k][3]);
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t f = e4m3x2_to_f16x2(sb[k]);
+                // lanes 2, 3 of a key write their chunks in another order: no two of a phase on the same banks
+                const uint32_t f0 = __byte_perm(f, f, hi ? 0x3232 : 0x1010), f1 = __byte_perm(f, f, hi ? 0x1010 : 0x3232);
+#pragma unroll
+                for (int q = 0; q < W; ++q) {
+                  uint32_t h[4];
+                  e2m1x8(W == 4 && hi ? cw[k][(q ^ 2) % W] : cw[k][q], h);
+                  const int chunk = W == 4 ? 4 * (c4 & 1) + (q ^ (c4 & 2)) : 2 * c4 + q;
+                  const uint32_t fq = W == 4 && q >= 2 ? f1 : f0;
+                  st_shared_v4(row + k * 32 * 128 + ((chunk ^ (key0 & 7)) << 4), hmul2(h[0], fq), hmul2(h[1], fq),
+                               hmul2(h[2], fq), hmul2(h[3], fq));
+                }
+              }
+            } else if (D == 128 || w < 2) {
+              // thread = (8 keys, block of 16 values)
+              const int first = tgh * 64 + tg * 8;
+              const int in = first & (p.P - 1);
+              const uint8_t* vc = ring + half_of(first) + in * (D / 2) + 8 * blk;
+              const uint8_t* vs = ring + half_of(first) + codes_bytes(p.P, D) + in * (D / 16) + blk;
+              // register q holds key q ^ odd, so that neighbours read different banks
+              const uint8_t *vc0 = vc + odd * (D / 2), *vc1 = vc - odd * (D / 2);
+              uint2 cw[8];
+              uint32_t sb[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                cw[q] = *reinterpret_cast<const uint2*>((q & 1 ? vc1 : vc0) + q * (D / 2));
+                sb[q] = vs[q * (D / 16)];
+              }
+              const int keys = it.len - (it.u + (i >> 1)) * kKeys - first;  // of the 8 that were written
+              if (keys < 8) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                  if (q >= keys) sb[q] = 0u;
+              }
+              uint32_t f[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) f[q] = e4m3x2_to_f16x2(sb[2 * q] | (sb[2 * q + 1] << 8));
+              const uint32_t vt = sv + st * C::K_BYTES + tgh * C::SUB_V + 16 * blk * 128;
+#pragma unroll
+              for (int v = 0; v < 2; ++v) {
+                uint32_t h[8][4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const uint32_t x = v ? cw[2 * q].y : cw[2 * q].x, y = v ? cw[2 * q + 1].y : cw[2 * q + 1].x;
+                  const uint32_t a = odd ? y : x, b = odd ? x : y;
+                  uint32_t even[4], odds[4];
+                  e2m1x8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even);
+                  e2m1x8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odds);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    h[2 * k][q] = hmul2(even[k], f[q]);
+                    h[2 * k + 1][q] = hmul2(odds[k], f[q]);
+                  }
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                  st_shared_v4(vt + (8 * v + k) * 128 + ((tg ^ k) << 4), h[k][0], h[k][1], h[k][2], h[k][3]);
+              }
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(is_v ? &bars.vfull[st] : &bars.kfull[st]);
+            for (int pg = 0; pg < pages; ++pg) {
+              if (lane == 0) mbar_arrive(&bars.empty[slot]);
+              if (++slot == slots) slot = 0, round ^= 1;
+            }
+            j += is_v;
           }
-          __syncwarp();
-          if (lane == 0)
-            for (int pg = 0; pg < pages; ++pg) mbar_arrive(&bars.empty[(s + pg) % slots]);
-          s += pages;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bars.vfull[st]);
         }
       } else if (warp == kLoad) {
         // ================================================================ load
-        Tiles t(p, x0, x1);
-        uint32_t s = 0;
-        for (; t.left > 0; t.next(p)) {
-          int page = -1;
-          const int at = t.c.u * pages + lane;
-          if (lane < pages && static_cast<long long>(at) * p.P < t.c.s.len) {
-            page = __ldg(p.table + static_cast<long long>(t.c.b) * p.max_pages + at);
-            if (page < 0 || page >= p.num_pages) {
-              atomicOr(p.err, kErrBadIndex);
-              page = 0;
+        int slot = 0;
+        uint32_t round = 0;  // times round the ring
+        ItemReader items;
+        while (true) {
+          const Item it = items.next(bars.items, tmo, p.err, abort);
+          if (it.n == 0) break;
+          const uint8_t* pool = p.pool + static_cast<long long>(it.h) * 2 * half;
+          const long long stride = static_cast<long long>(p.Hkv) * 2 * half;
+          const int32_t* table = p.table + static_cast<long long>(it.b) * p.max_pages;
+          // page ids of the next 32 pages, one per lane
+          const int first = it.u * pages, last = min((it.u + it.n) * pages, (it.len + p.P - 1) / p.P);
+          int ids = -1;
+          for (int k = 0; k < 2 * pages * it.n; ++k) {
+            const int tile = k / (2 * pages), in = k & (2 * pages - 1);
+            const int pg = tile * pages + (in & (pages - 1));  // in the item
+            if (in == 0 && (pg & 31) == 0) {
+              ids = -1;
+              if (first + pg + lane < last) {
+                ids = __ldg(table + first + pg + lane);
+                if (ids < 0 || ids >= p.num_pages) {
+                  atomicOr(p.err, kErrBadIndex);
+                  ids = 0;
+                }
+              }
             }
-          }
-          for (int k = 0; k < 2 * pages; ++k, ++s) {
-            const int pg = __shfl_sync(0xFFFFFFFFu, page, k % pages);
-            const uint32_t slot = s % slots;
+            const int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
+            if (round > 0) wait_warp(&bars.empty[slot], (round - 1) & 1, tmo, p.err, abort);
             if (lane == 0) {
-              if (s >= static_cast<uint32_t>(slots))
-                mbar_wait_bounded(&bars.empty[slot], (s / slots - 1) & 1, tmo, p.err, &bars.abort);
-              if (pg < 0 || *static_cast<volatile int*>(&bars.abort)) {
-                mbar_arrive(&bars.full[slot]);  // no key of this tile
+              if (id < 0 || *static_cast<volatile int*>(abort)) {
+                mbar_arrive(&bars.full[slot]);  // no key of this page
               } else {
                 mbar_arrive_expect_tx(&bars.full[slot], half);
-                bulk_load(ring + slot * half,
-                          p.pool + (static_cast<long long>(pg) * p.Hkv + t.c.h) * 2 * half + (k < pages ? 0 : half), half,
-                          &bars.full[slot]);
+                bulk_load(ring + slot * half, pool + id * stride + (in < pages ? 0 : half), half, &bars.full[slot]);
               }
             }
             __syncwarp();
+            if (++slot == slots) slot = 0, ++round;
           }
         }
         // after a time-out elsewhere, stay until the copies in flight have landed
-        if (*static_cast<volatile int*>(&bars.abort) && lane == 0)
-          for (uint32_t k = s > static_cast<uint32_t>(slots) ? s - slots : 0; k < s; ++k)
-            mbar_wait_bounded(&bars.full[k % slots], (k / slots) & 1, tmo, p.err, nullptr);
-      } else if (warp == kMma || warp == kWait) {
-        // ========================================== matrix instructions / waits
-        // Both warps walk the same steps; the waiting warp lets the other one
-        // through a named barrier when a step's operands are there.
-        const bool issue = warp == kMma;
-        const uint64_t dq[2] = {smem_desc_kmajor_sw128(sq), smem_desc_kmajor_sw128(sq + C::Q_BYTES)};
-        const uint64_t dk = smem_desc_kmajor_sw128(sk), dv = smem_desc_kmajor_sw128(sv);
-        uint32_t nq[2] = {0, 0}, np[2] = {0, 0};  // items' queries and P tiles taken, per row tile
-        auto go = [&]() {
-          named_bar_sync(1, 64);
-          if (issue) tc_fence_after();
-        };
-        auto score = [&](int g, uint32_t j, bool first, bool last_use) {  // S_g = Q_g K(j)^T
-          if (!issue) {
-            if (first) mbar_wait_warp(&bars.qfull[g], nq[g] & 1, tmo, p.err, &bars.abort);
-            if (g == 0) mbar_wait_warp(&bars.kfull[j & 1], (j >> 1) & 1, tmo, p.err, &bars.abort);
-          }
-          if (first) ++nq[g];
-          go();
-          if (issue) {
-            const uint64_t b = dk + (j & 1) * (C::K_BYTES >> 4);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
-              umma_f16_ss_warp(tmem + g * 128, dq[g] + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
-            }
-            umma_commit_warp(&bars.sfull[g]);
-            if (last_use) umma_commit_warp(&bars.kempty[j & 1]);
-          }
-        };
-        auto value = [&](int g, uint32_t j, bool first, bool last_use) {  // O_g += P_g V(j)
-          if (!issue) {
-            if (g == 0) mbar_wait_warp(&bars.vfull[j & 1], (j >> 1) & 1, tmo, p.err, &bars.abort);
-            mbar_wait_warp(&bars.pfull[g], np[g] & 1, tmo, p.err, &bars.abort);
-          }
-          ++np[g];
-          go();
-          if (issue) {
-            const uint64_t b = dv + (j & 1) * (C::K_BYTES >> 4);
-#pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_f16_ts_warp(tmem + 256 + g * 128, tmem + g * 128 + 8 * kk, b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2,
-                               idesc_f16_f32(128, D), first && kk == 0 ? 0u : 1u);
-            umma_commit_warp(&bars.ofull[g]);
-            if (last_use) umma_commit_warp(&bars.vempty[j & 1]);
-          }
-        };
-        Tiles t(p, x0, x1);
-        score(0, 0, true, !t.two);
-        if (t.two) score(1, 0, true, true);
-        for (uint32_t j = 0; t.left > 0; ++j) {
-          const bool two = t.two, first = t.first;
-          value(0, j, first, !two);
-          t.next(p);
-          if (t.left > 0) score(0, j + 1, t.first, !t.two);
-          if (two) value(1, j, first, true);
-          if (t.left > 0 && t.two) score(1, j + 1, t.first, true);
+        if (*static_cast<volatile int*>(abort) && lane == 0)
+          for (int k = 0; k < slots; ++k)  // the last use of each slot
+            if (k < slot || round > 0)
+              mbar_wait_bounded(&bars.full[k], (k < slot ? round : round - 1) & 1, tmo, p.err, nullptr, true);
+      } else if (warp == kWalk) {
+        // ================================================================ walk
+        Cursor c = cursor_at<kRows>(p, kKeys, x0);
+        ItemWriter out;
+        long long left = x1 - x0;
+        while (!*static_cast<volatile int*>(abort)) {
+          const int n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
+          out.put(bars.items, make_item<kRows>(p, c, n, blockIdx.x), tmo, p.err, abort);
+          if (left <= 0) break;  // that was the end mark
+          left -= n;
+          if (left > 0) cursor_next<kRows>(p, kKeys, c);
         }
+      } else {
+        // ========================================== matrix instructions / waits
+        // Both warps walk the same steps: P_A V, Q_A K', P_B V, Q_B K'.  The
+        // waiting warp lets the other one through a named barrier when a
+        // step's operands are there; either one can end both.
+        const bool issue = warp == kMma;
+        const uint64_t dq = smem_desc_kmajor_sw128(sq), dk = smem_desc_kmajor_sw128(sk), dv = smem_desc_kmajor_sw128(sv);
+        uint32_t pq = 0, pp = 0;  // parities of qfull and pfull, bit g
+        ItemReader items;
+        Item nx = items.next(bars.items, tmo, p.err, abort);
+        int rem = nx.n;
+        bool nx_first = true, cur = false, cur_two = false, cur_first = false, stop = false;
+        for (uint32_t j = 0;; ++j) {  // value of tile j - 1, scores of tile j
+          const bool more = rem > 0, nx_two = nx.rows > 128;
+#pragma unroll 1
+          for (int g = 0; g < 2 && !stop; ++g) {
+            if (cur && (g == 0 || cur_two)) {  // O_g += P_g V(j - 1)
+              const uint32_t st = (j - 1) & 1;
+              if (!issue) {
+                if (g == 0) wait_warp(&bars.vfull[st], ((j - 1) >> 1) & 1, tmo, p.err, abort);
+                wait_warp(&bars.pfull[g], (pp >> g) & 1, tmo, p.err, abort);
+              }
+              pp ^= 1u << g;
+              stop = named_bar_red_or(1, 64, *static_cast<volatile int*>(abort) != 0);
+              if (stop) break;
+              if (issue) {
+                tc_fence_after();
+                const uint64_t b = dv + st * (C::K_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                  umma_f16_ts_warp(tmem + 256 + g * 128, tmem + g * 128 + 8 * kk,
+                                   b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
+                                   cur_first && kk == 0 ? 0u : 1u);
+                umma_commit_warp(&bars.ofull[g]);
+                if (g == 1 || !cur_two) umma_commit_warp(&bars.vempty[st]);
+              }
+            }
+            if (more && (g == 0 || nx_two)) {  // S_g = Q_g K(j)^T
+              const uint32_t st = j & 1;
+              if (!issue) {
+                if (nx_first) wait_warp(&bars.qfull[g], (pq >> g) & 1, tmo, p.err, abort);
+                if (g == 0) wait_warp(&bars.kfull[st], (j >> 1) & 1, tmo, p.err, abort);
+              }
+              if (nx_first) pq ^= 1u << g;
+              stop = named_bar_red_or(1, 64, *static_cast<volatile int*>(abort) != 0);
+              if (stop) break;
+              if (issue) {
+                tc_fence_after();
+                const uint64_t a = dq + g * (C::Q_BYTES >> 4), b = dk + st * (C::K_BYTES >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
+                  umma_f16_ss_warp(tmem + g * 128, a + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
+                }
+                umma_commit_warp(&bars.sfull[g]);
+                if (g == 1 || !nx_two) umma_commit_warp(&bars.kempty[st]);
+              }
+            }
+          }
+          if (stop) break;
+          cur = more, cur_two = nx_two, cur_first = nx_first;
+          if (!cur) break;
+          nx_first = false;
+          if (--rem == 0) {
+            nx = items.next(bars.items, tmo, p.err, abort);
+            rem = nx.n;
+            nx_first = true;
+          }
+        }
+        // One that saw the time-out as an end of the items meets the other here.
+        if (!stop) named_bar_red_or(1, 64, true);
         if (issue) {
           umma_commit_warp(&bars.done);
-          mbar_wait_warp(&bars.done, 0, tmo, p.err, nullptr);
+          mbar_wait_warp(&bars.done, 0, 1000000000ull, p.err, nullptr);
         }
       }
     }
