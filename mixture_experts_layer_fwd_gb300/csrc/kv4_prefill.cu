@@ -7,17 +7,17 @@
 //
 //   0-3, 4-7  softmax of tile A / B, one row per thread: S from tensor memory,
 //             running maximum and sum, P (fp16) back over S's columns
-//   8-11      expand the codes: K as [key][d], V transposed to [d][key], both
-//             fp16 in the 128-byte swizzle the matrix instructions read
-//   12        bulk copies of the halves (keys, values) of page records
-//   13        issues the matrix instructions, 14 waits for it (a wait in the
+//   8-11      expand the codes of K as [key][d], 12-15 those of V transposed
+//             to [d][key], fp16 in the swizzle the matrix instructions read
+//   16        bulk copies of the halves (keys, values) of page records
+//   17        issues the matrix instructions, 18 waits for it (a wait in the
 //             issuing warp would queue behind its instructions)
-//   15        walks the block's items and publishes them to the others
+//   19        walks the block's items and publishes them to the others
 //
 // S = Q K^T comes from shared memory, O += P V takes P from tensor memory.  The
 // order of issue is P_A V, Q_A K', P_B V, Q_B K' (K' the next tile), so that
 // one tile's softmax runs under the other's products.  S and O fill tensor
-// memory: 2 x 128 + 2 x D columns; P lies in the first half of its S.
+// memory: 2 x 128 + 2 x D columns; P lies in the second half of its S.
 //
 // The running maximum is moved only when a row's grows by more than 2^kSlack:
 // until then O needs no rescaling, and P keeps fp16's relative precision.
@@ -31,10 +31,10 @@ namespace {
 
 constexpr int kRows = kRowsTile;
 constexpr int kKeys = 128;
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;  // at 96 registers; shared out as 256 x 136, 256 x 72, 128 x 64
 constexpr int kMaxSlots = 16;
-constexpr int kExpand0 = 8, kLoad = 12, kMma = 13, kWalk = 15;  // 14 waits for 13
-constexpr int kReaders = 8 + 4 + 3;
+constexpr int kExpandV = 12, kLoad = 16, kMma = 17, kWalk = 19;  // 18 waits for 17
+constexpr int kReaders = 8 + 8 + 3;
 
 template <int D>
 struct Cfg {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
   if (x0 < x1) {
     if (warp < 8) {
       // ================================================================ softmax
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
       const int g = warp >> 2;                       // tile A or B
       const int r = (warp & 3) * 32 + lane;          // row in the tile
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -229,32 +229,47 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           for (int i = 0; i < it.n; ++i, ++cnt) {
             wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, abort);
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(ts + 32 * q, s[q]);
-            tmem_ld_wait();
             const int a = lo - (it.u + i) * kKeys, b = hi - (it.u + i) * kKeys;  // the row's keys, in the tile
-            if (!__all_sync(0xFFFFFFFFu, a <= 0 && b >= kKeys)) {
-#pragma unroll
+            if (!__all_sync(0xFFFFFFFFu, a <= 0 && b >= kKeys)) {  // some row does not see all of these keys
+#pragma unroll 1
               for (int q = 0; q < 4; ++q) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(ts + 32 * q, v);
+                tmem_ld_wait();
                 // bit j: key 32 q + j is seen
                 const int x = min(max(a - 32 * q, 0), 32), y = min(max(b - 32 * q, 0), 32);
                 const uint32_t see = static_cast<uint32_t>(((1ull << y) - 1ull) & ~((1ull << x) - 1ull));
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                  if (!(see & (1u << j))) s[q][j] = 0xFF800000u;  // -infinity
+                  if (!(see & (1u << j))) v[j] = 0xFF800000u;  // -infinity
+                tmem_st_32x32b_x32(ts + 32 * q, v);
               }
+              tmem_st_wait();
             }
-            float mx[4];
+            auto largest = [&](const uint32_t (&v)[32], float x) {
+              float y = __uint_as_float(v[0]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              mx[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-              for (int j = 1; j < 31; j += 2)
-                mx[q] = fmaxf(fmaxf(mx[q], __uint_as_float(s[q][j])), __uint_as_float(s[q][j + 1]));
-              mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
+              for (int j = 1; j < 29; j += 4) {
+                x = fmaxf(fmaxf(x, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+                y = fmaxf(fmaxf(y, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
+              }
+              x = fmaxf(fmaxf(x, __uint_as_float(v[29])), __uint_as_float(v[30]));
+              return fmaxf(fmaxf(x, y), __uint_as_float(v[31]));
+            };
+            // S is read twice, 32 keys at a time, the next ones on their way
+            uint32_t va[32], vb[32];
+            float top = -INFINITY;
+            tmem_ld_32x32b_x32(ts, va);
+#pragma unroll 1
+            for (int q = 0; q < 4; q += 2) {
+              tmem_ld_wait();
+              tmem_ld_32x32b_x32(ts + 32 * (q + 1), vb);
+              top = largest(va, top);
+              tmem_ld_wait();
+              tmem_ld_32x32b_x32(ts + 32 * (q ? 3 : 2), va);  // the second time round: keys 96 .. 127 again
+              top = largest(vb, top);
             }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sc;
+            top *= sc;
             const bool grow = top > m + kSlack;  // also the row's first keys
             if (__any_sync(0xFFFFFFFFu, grow)) {
               float f = 1.0f;
@@ -281,19 +296,28 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               }
             }
             const uint64_t sc2 = pair(sc, sc), nb2 = pair(nb, nb);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            auto weigh = [&](int q, const uint32_t (&v)[32]) {  // P of 32 keys
               uint32_t w[16];
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 float x, y;
-                unpair(fma2(pair(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), sc2, nb2), x, y);
+                unpair(fma2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sc2, nb2), x, y);
                 x = ex2(x);
                 y = ex2(y);
                 l2[j & 1] = add2(l2[j & 1], pair(x, y));
                 w[j] = pack_f16x2(x, y);
               }
-              tmem_st_32x32b_x16(ts + 16 * q, w);
+              tmem_st_32x32b_x16(ts + 64 + 16 * q, w);
+            };
+            // from the last keys on: P's columns lie over keys already taken
+#pragma unroll 1
+            for (int q = 3; q > 0; q -= 2) {
+              tmem_ld_wait();
+              tmem_ld_32x32b_x32(ts + 32 * (q - 1), vb);
+              weigh(q, va);
+              tmem_ld_wait();
+              if (q > 1) tmem_ld_32x32b_x32(ts + 32 * (q - 2), va);
+              weigh(q - 1, vb);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -304,16 +328,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         nx = items.next(bars.items, tmo, p.err, abort);
       }
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
       if (warp < kLoad) {
         // ============================================================== expand
-        const int w = warp - kExpand0, c4 = lane & 3;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const bool is_v = warp >= kExpandV;
+        const int w = warp & 3, c4 = lane & 3;
         const int tg = lane & 7, tgh = w & 1;  // V: group of 8 keys in a 64-key sub-tile
         const int blk = D == 128 ? (2 * (tg >> 1) + (lane >> 3) + 4 * (w >> 1)) & 7 : (2 * (tg >> 1) + (lane >> 3)) & 3;
         const int odd = tg & 1;
         const int logp = p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
-        int slot = 0;        // of the ring's next half
-        uint32_t round = 0;  // its parity
+        int slot = is_v ? pages : 0;  // of the ring's next half for these warps: K and V halves take turns
+        uint32_t round = 0;           // its parity
         // Byte offset of a key's half, the key counted in the tile.
         auto half_of = [&](int key) {
           int sl = slot + (key >> logp);
@@ -325,8 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         while (true) {
           const Item it = items.next(bars.items, tmo, p.err, abort);
           if (it.n == 0) break;
-          for (int i = 0; i < 2 * it.n; ++i) {  // K, V, K, V, ...
-            const bool is_v = i & 1;
+          for (int i = 0; i < it.n; ++i, ++j) {
             const uint32_t st = j & 1, ph = (j >> 1) & 1;
             {
               int sl = slot;
@@ -340,13 +364,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             if (!is_v) {
               // lane = (key, quarter of its values); the warp's keys are 32k + 8w ..
               constexpr int W = D / 32;  // words of 8 codes per lane
-              uint32_t cw[4][W], sb[4];
               const bool hi = W == 4 && (c4 & 2);
               const int key0 = 8 * w + (lane >> 2);
+#pragma unroll 1
+             for (int k2 = 0; k2 < 4; k2 += 2) {
+              uint32_t cw[2][W], sb[2];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int in = (32 * k + key0) & (p.P - 1);
-                const uint8_t* kc = ring + half_of(32 * k);
+              for (int k = 0; k < 2; ++k) {
+                const int in = (32 * (k2 + k) + key0) & (p.P - 1);
+                const uint8_t* kc = ring + half_of(32 * (k2 + k));
                 if (W == 4) {
                   const uint4 v = *reinterpret_cast<const uint4*>(kc + in * (D / 2) + 16 * c4);
                   cw[k][0] = v.x, cw[k][1] = v.y, cw[k][2 % W] = v.z, cw[k][3 % W] = v.w;
@@ -357,9 +383,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                   sb[k] = kc[codes_bytes(p.P, D) + in * (D / 16) + c4];
                 }
               }
-              const uint32_t row = sk + st * C::K_BYTES + (W == 4 ? (c4 >> 1) * C::SUB_Q : 0) + key0 * 128;
+              const uint32_t row = sk + st * C::K_BYTES + (W == 4 ? (c4 >> 1) * C::SUB_Q : 0) + (32 * k2 + key0) * 128;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
+              for (int k = 0; k < 2; ++k) {
                 const uint32_t f = e4m3x2_to_f16x2(sb[k]);
                 // lanes 2, 3 of a key write their chunks in another order: no two of a phase on the same banks
                 const uint32_t f0 = __byte_perm(f, f, hi ? 0x3232 : 0x1010), f1 = __byte_perm(f, f, hi ? 0x1010 : 0x3232);
@@ -373,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                                hmul2(h[2], fq), hmul2(h[3], fq));
                 }
               }
+             }
             } else if (D == 128 || w < 2) {
               // thread = (8 keys, block of 16 values)
               const int first = tgh * 64 + tg * 8;
@@ -388,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 cw[q] = *reinterpret_cast<const uint2*>((q & 1 ? vc1 : vc0) + q * (D / 2));
                 sb[q] = vs[q * (D / 16)];
               }
-              const int keys = it.len - (it.u + (i >> 1)) * kKeys - first;  // of the 8 that were written
+              const int keys = it.len - (it.u + i) * kKeys - first;  // of the 8 that were written
               if (keys < 8) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q)
@@ -422,14 +449,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(is_v ? &bars.vfull[st] : &bars.kfull[st]);
-            for (int pg = 0; pg < pages; ++pg) {
-              if (lane == 0) mbar_arrive(&bars.empty[slot]);
+            for (int pg = 0; pg < 2 * pages; ++pg) {
+              if (pg < pages && lane == 0) mbar_arrive(&bars.empty[slot]);
               if (++slot == slots) slot = 0, round ^= 1;
             }
-            j += is_v;
           }
         }
-      } else if (warp == kLoad) {
+      } else {
+       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+       if (warp == kLoad) {
         // ================================================================ load
         int slot = 0;
         uint32_t round = 0;  // times round the ring
@@ -517,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 const uint64_t b = dv + st * (C::K_BYTES >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kKeys / 16; ++kk)
-                  umma_f16_ts_warp(tmem + 256 + g * 128, tmem + g * 128 + 8 * kk,
+                  umma_f16_ts_warp(tmem + 256 + g * 128, tmem + g * 128 + 64 + 8 * kk,
                                    b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
                                    cur_first && kk == 0 ? 0u : 1u);
                 umma_commit_warp(&bars.ofull[g]);
@@ -562,6 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           umma_commit_warp(&bars.done);
           mbar_wait_warp(&bars.done, 0, 1000000000ull, p.err, nullptr);
         }
+       }
       }
     }
   }
