@@ -254,15 +254,22 @@ DEVINL void item_keys(const AttnParams& p, const Item& t, int idx, int& lo, int&
 }
 
 // Bounded wait of a whole warp, every lane testing: mbar_wait_bounded's rules.
+// The test suspends the warp in hardware for a while by itself (a given
+// suspend time makes it sleep in steps that cost a round trip each: measured
+// 1.33 against 1.22 ms on a 4096-token chunk at 12289 keys); the clock is
+// read once in 64 tests.
 DEVINL void wait_warp(uint64_t* bar, uint32_t parity, unsigned long long tmo, unsigned int* err, volatile int* abort) {
-  uint64_t t0 = 0;
-  while (!mbar_try_wait_suspend(bar, parity, 20000u)) {
-    const uint64_t now = globaltimer_ns();
-    if (t0 == 0) t0 = now;
-    if (*abort || now - t0 > tmo) {
-      atomicOr(err, kErrTimeout);
-      *abort = 1;
-      break;
+  if (!mbar_try_wait(bar, parity)) {
+    uint64_t t0 = 0;
+    for (uint32_t k = 1; !mbar_try_wait(bar, parity); ++k) {
+      if (k & 63u) continue;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (*abort || now - t0 > tmo) {
+        atomicOr(err, kErrTimeout);
+        *abort = 1;
+        break;
+      }
     }
   }
   __syncwarp();

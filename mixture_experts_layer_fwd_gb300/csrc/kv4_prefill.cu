@@ -10,13 +10,14 @@
 //   8-11      expand the codes of K as [key][d], 12-15 those of V transposed
 //             to [d][key], fp16 in the swizzle the matrix instructions read
 //   16        bulk copies of the halves (keys, values) of page records
-//   17        issues the matrix instructions, 18 waits for it (a wait in the
-//             issuing warp would queue behind its instructions)
+//   17, 18    issue the matrix instructions of tile A / B
 //   19        walks the block's items and publishes them to the others
 //
-// S = Q K^T comes from shared memory, O += P V takes P from tensor memory.  The
-// order of issue is P_A V, Q_A K', P_B V, Q_B K' (K' the next tile), so that
-// one tile's softmax runs under the other's products.  S and O fill tensor
+// S = Q K^T comes from shared memory, O += P V takes P from tensor memory.  One
+// tile's softmax runs under the other's products, and so does the time from a
+// barrier to the first instruction after it (about 450 cycles; with one warp
+// issuing for both tiles it came four times per tile of keys and left the
+// tensor cores idle half the time: 1.22 ms against 0.XX).  S and O fill tensor
 // memory: 2 x 128 + 2 x D columns; P lies in the second half of its S.
 //
 // The running maximum is moved only when a row's grows by more than 2^kSlack:
@@ -33,7 +34,7 @@ constexpr int kRows = kRowsTile;
 constexpr int kKeys = 128;
 constexpr int kThreads = 640;  // at 96 registers; shared out as 256 x 136, 256 x 72, 128 x 64
 constexpr int kMaxSlots = 16;
-constexpr int kExpandV = 12, kLoad = 16, kMma = 17, kWalk = 19;  // 18 waits for 17
+constexpr int kExpandV = 12, kLoad = 16, kMma = 17, kWalk = 19;
 constexpr int kReaders = 8 + 8 + 3;
 
 template <int D>
@@ -49,7 +50,7 @@ struct Cfg {
 struct Bars {
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t qfull[2], sfull[2], pfull[2], ofull[2], done;
+  uint64_t qfull[2], sfull[2], pfull[2], ofull[2], turn[2], done;
   ItemRing items;
   uint32_t tmem;
   int abort;
@@ -123,15 +124,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.kfull[i], 4);
-      mbar_init(&bars.kempty[i], 1);
+      mbar_init(&bars.kempty[i], 2);
       mbar_init(&bars.vfull[i], 4);
-      mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.vempty[i], 2);
       mbar_init(&bars.qfull[i], 4);
       mbar_init(&bars.sfull[i], 1);
       mbar_init(&bars.pfull[i], 4);
       mbar_init(&bars.ofull[i], 1);
+      mbar_init(&bars.turn[i], 1);
     }
-    mbar_init(&bars.done, 1);
+    mbar_init(&bars.done, 2);
     item_ring_init(bars.items, kReaders);
     bars.abort = 0;
     fence_mbar_init();
@@ -459,8 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
        if (warp == kLoad) {
         // ================================================================ load
-        int slot = 0;
-        uint32_t round = 0;  // times round the ring
+        // Lane l feeds slot l, each at its own pace: one thread for all slots
+        // took about 900 cycles per copy, in waits and barrier round trips.
+        uint32_t uses = 0;  // of the lane's slot
+        int at = 0;         // slot of the item's first half
         ItemReader items;
         while (true) {
           const Item it = items.next(bars.items, tmo, p.err, abort);
@@ -468,41 +472,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           const uint8_t* pool = p.pool + static_cast<long long>(it.h) * 2 * half;
           const long long stride = static_cast<long long>(p.Hkv) * 2 * half;
           const int32_t* table = p.table + static_cast<long long>(it.b) * p.max_pages;
-          // page ids of the next 32 pages, one per lane
-          const int first = it.u * pages, last = min((it.u + it.n) * pages, (it.len + p.P - 1) / p.P);
-          int ids = -1;
-          for (int k = 0; k < 2 * pages * it.n; ++k) {
-            const int tile = k / (2 * pages), in = k & (2 * pages - 1);
-            const int pg = tile * pages + (in & (pages - 1));  // in the item
-            if (in == 0 && (pg & 31) == 0) {
-              ids = -1;
-              if (first + pg + lane < last) {
-                ids = __ldg(table + first + pg + lane);
-                if (ids < 0 || ids >= p.num_pages) {
-                  atomicOr(p.err, kErrBadIndex);
-                  ids = 0;
+          const int first = it.u * pages, last = (it.len + p.P - 1) / p.P, all = 2 * pages * it.n;
+          const int shift = pages == 1 ? 1 : pages == 2 ? 2 : 3;  // halves of a tile: keys of its pages, then values
+          int k = lane < slots ? (lane >= at ? lane - at : lane - at + slots) : all;
+          int id = -2;  // page of half k: -2 not looked up, -1 none
+          uint64_t t0 = 0;
+          for (uint32_t spin = 1; __any_sync(0xFFFFFFFFu, k < all); ++spin) {
+            if (k < all) {
+              const int in = k & (2 * pages - 1);
+              if (id == -2) {
+                const int pg = first + (k >> shift) * pages + (in & (pages - 1));
+                id = -1;
+                if (pg < last) {
+                  id = __ldg(table + pg);
+                  if (id < 0 || id >= p.num_pages) {
+                    atomicOr(p.err, kErrBadIndex);
+                    id = 0;
+                  }
                 }
               }
-            }
-            const int id = __shfl_sync(0xFFFFFFFFu, ids, pg & 31);
-            if (round > 0) wait_warp(&bars.empty[slot], (round - 1) & 1, tmo, p.err, abort);
-            if (lane == 0) {
-              if (id < 0 || *static_cast<volatile int*>(abort)) {
-                mbar_arrive(&bars.full[slot]);  // no key of this page
-              } else {
-                mbar_arrive_expect_tx(&bars.full[slot], half);
-                bulk_load(ring + slot * half, pool + id * stride + (in < pages ? 0 : half), half, &bars.full[slot]);
+              if (uses == 0 || mbar_test_wait(&bars.empty[lane], (uses - 1) & 1)) {
+                if (id < 0) {
+                  mbar_arrive(&bars.full[lane]);  // no key of this page
+                } else {
+                  mbar_arrive_expect_tx(&bars.full[lane], half);
+                  bulk_load(ring + lane * half, pool + id * stride + (in < pages ? 0 : half), half, &bars.full[lane]);
+                }
+                ++uses;
+                k += slots;
+                id = -2;
               }
             }
-            __syncwarp();
-            if (++slot == slots) slot = 0, ++round;
+            if ((spin & 255u) == 0u) {
+              const uint64_t now = globaltimer_ns();
+              if (t0 == 0) t0 = now;
+              const bool late = now - t0 > tmo && k < all && uses > 0 && !mbar_test_wait(&bars.empty[lane], (uses - 1) & 1);
+              if (__any_sync(0xFFFFFFFFu, late)) {
+                atomicOr(p.err, kErrTimeout);
+                *static_cast<volatile int*>(abort) = 1;
+              }
+              if (*static_cast<volatile int*>(abort)) break;
+            } else if (spin & 1u) {
+              t0 = __any_sync(0xFFFFFFFFu, id == -2) ? 0 : t0;  // something moved
+            }
           }
+          at = (at + all) % slots;
+          if (*static_cast<volatile int*>(abort)) break;
         }
         // after a time-out elsewhere, stay until the copies in flight have landed
-        if (*static_cast<volatile int*>(abort) && lane == 0)
-          for (int k = 0; k < slots; ++k)  // the last use of each slot
-            if (k < slot || round > 0)
-              mbar_wait_bounded(&bars.full[k], (k < slot ? round : round - 1) & 1, tmo, p.err, nullptr, true);
+        if (*static_cast<volatile int*>(abort) && uses > 0)
+          mbar_wait_bounded(&bars.full[lane], (uses - 1) & 1, tmo, p.err, nullptr, true);
       } else if (warp == kWalk) {
         // ================================================================ walk
         Cursor c = cursor_at<kRows>(p, kKeys, x0);
@@ -516,80 +535,73 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           if (left > 0) cursor_next<kRows>(p, kKeys, c);
         }
       } else {
-        // ========================================== matrix instructions / waits
-        // Both warps walk the same steps: P_A V, Q_A K', P_B V, Q_B K'.  The
-        // waiting warp lets the other one through a named barrier when a
-        // step's operands are there; either one can end both.
-        const bool issue = warp == kMma;
-        const uint64_t dq = smem_desc_kmajor_sw128(sq), dk = smem_desc_kmajor_sw128(sk), dv = smem_desc_kmajor_sw128(sv);
-        uint32_t pq = 0, pp = 0;  // parities of qfull and pfull, bit g
+        // =================================================== matrix instructions
+        // Warp kMma issues tile A's, kMma + 1 tile B's: what one waits for is
+        // hidden under the other's.  Per tile of keys: all waits, then
+        // O_g += P_g V(j - 1) and S_g = Q_g K(j)^T back to back.
+        const int g = warp - kMma;
+        const uint64_t dq = smem_desc_kmajor_sw128(sq + g * C::Q_BYTES);
+        const uint64_t dk = smem_desc_kmajor_sw128(sk), dv = smem_desc_kmajor_sw128(sv);
+        const uint32_t ts = tmem + g * 128, to = tmem + 256 + g * 128;
+        uint32_t pq = 0, pp = 0;  // parities of qfull and pfull
         ItemReader items;
         Item nx = items.next(bars.items, tmo, p.err, abort);
         int rem = nx.n;
-        bool nx_first = true, cur = false, cur_two = false, cur_first = false, stop = false;
-        for (uint32_t j = 0;; ++j) {  // value of tile j - 1, scores of tile j
-          const bool more = rem > 0, nx_two = nx.rows > 128;
-#pragma unroll 1
-          for (int g = 0; g < 2 && !stop; ++g) {
-            if (cur && (g == 0 || cur_two)) {  // O_g += P_g V(j - 1)
-              const uint32_t st = (j - 1) & 1;
-              if (!issue) {
-                if (g == 0) wait_warp(&bars.vfull[st], ((j - 1) >> 1) & 1, tmo, p.err, abort);
-                wait_warp(&bars.pfull[g], (pp >> g) & 1, tmo, p.err, abort);
-              }
-              pp ^= 1u << g;
-              stop = named_bar_red_or(1, 64, *static_cast<volatile int*>(abort) != 0);
-              if (stop) break;
-              if (issue) {
-                tc_fence_after();
-                const uint64_t b = dv + st * (C::K_BYTES >> 4);
-#pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                  umma_f16_ts_warp(tmem + 256 + g * 128, tmem + g * 128 + 64 + 8 * kk,
-                                   b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
-                                   cur_first && kk == 0 ? 0u : 1u);
-                umma_commit_warp(&bars.ofull[g]);
-                if (g == 1 || !cur_two) umma_commit_warp(&bars.vempty[st]);
-              }
-            }
-            if (more && (g == 0 || nx_two)) {  // S_g = Q_g K(j)^T
-              const uint32_t st = j & 1;
-              if (!issue) {
-                if (nx_first) wait_warp(&bars.qfull[g], (pq >> g) & 1, tmo, p.err, abort);
-                if (g == 0) wait_warp(&bars.kfull[st], (j >> 1) & 1, tmo, p.err, abort);
-              }
-              if (nx_first) pq ^= 1u << g;
-              stop = named_bar_red_or(1, 64, *static_cast<volatile int*>(abort) != 0);
-              if (stop) break;
-              if (issue) {
-                tc_fence_after();
-                const uint64_t a = dq + g * (C::Q_BYTES >> 4), b = dk + st * (C::K_BYTES >> 4);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                  const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
-                  umma_f16_ss_warp(tmem + g * 128, a + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
-                }
-                umma_commit_warp(&bars.sfull[g]);
-                if (g == 1 || !nx_two) umma_commit_warp(&bars.kempty[st]);
-              }
-            }
+        bool nx_first = true, cur = false, cur_mine = false, cur_first = false;
+        for (uint32_t j = 0; rem > 0 || cur; ++j) {
+          const uint32_t st = j & 1, so = st ^ 1;
+          const bool more = rem > 0, mine = more && nx.rows > g * 128;
+          if (more) wait_warp(&bars.kfull[st], (j >> 1) & 1, tmo, p.err, abort);
+          if (cur) wait_warp(&bars.vfull[so], ((j - 1) >> 1) & 1, tmo, p.err, abort);
+          if (cur_mine) {
+            wait_warp(&bars.pfull[g], pp, tmo, p.err, abort);
+            pp ^= 1;
           }
-          if (stop) break;
-          cur = more, cur_two = nx_two, cur_first = nx_first;
-          if (!cur) break;
+          if (mine && nx_first) {
+            wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
+            pq ^= 1;
+          }
+          // The tiles take turns, each after the other's products are done: left
+          // to themselves they fall into step, and the tensor cores idle while
+          // both are in their softmax.
+          if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, tmo, p.err, abort);
+          tc_fence_after();
+          if (cur_mine) {
+            const uint64_t b = dv + so * (C::K_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_f16_ts_warp(to, ts + 64 + 8 * kk, b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
+                               cur_first && kk == 0 ? 0u : 1u);
+            umma_commit_warp(&bars.ofull[g]);
+            umma_commit_warp(&bars.vempty[so]);
+          } else if (cur && lane == 0) {
+            mbar_arrive(&bars.vempty[so]);
+          }
+          if (mine) {
+            const uint64_t b = dk + st * (C::K_BYTES >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
+              umma_f16_ss_warp(ts, dq + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
+            }
+            umma_commit_warp(&bars.sfull[g]);
+            umma_commit_warp(&bars.kempty[st]);
+          } else if (more && lane == 0) {
+            mbar_arrive(&bars.kempty[st]);
+          }
+          if (cur_mine || mine) umma_commit_warp(&bars.turn[g ^ 1]);
+          else if (lane == 0) mbar_arrive(&bars.turn[g ^ 1]);
+          __syncwarp();
+          cur = more, cur_mine = mine, cur_first = nx_first;
           nx_first = false;
-          if (--rem == 0) {
+          if (more && --rem == 0) {
             nx = items.next(bars.items, tmo, p.err, abort);
             rem = nx.n;
             nx_first = true;
           }
         }
-        // One that saw the time-out as an end of the items meets the other here.
-        if (!stop) named_bar_red_or(1, 64, true);
-        if (issue) {
-          umma_commit_warp(&bars.done);
-          mbar_wait_warp(&bars.done, 0, 1000000000ull, p.err, nullptr);
-        }
+        umma_commit_warp(&bars.done);
+        mbar_wait_warp(&bars.done, 0, 1000000000ull, p.err, nullptr);
        }
       }
     }
