@@ -5,20 +5,20 @@
 // Bound: the tensor cores, 4 * 128 * D multiply-adds per row and tile of keys,
 // then the exponentials.  One block per SM; the roles, by warp:
 //
-//   0-3, 4-7  softmax of tile A / B, one row per thread: S from tensor memory,
-//             running maximum and sum, P (fp16) back over S's columns
-//   8-11      expand the codes of K as [key][d], 12-15 those of V transposed
+//   0-7, 8-15 softmax of tile A / B, half a row per thread: S from tensor
+//             memory, running maximum and sum, P (fp16) back over S's columns
+//   16-19     expand the codes of K as [key][d], 20-23 those of V transposed
 //             to [d][key], fp16 in the swizzle the matrix instructions read
-//   16        bulk copies of the halves (keys, values) of page records
-//   17, 18    issue the matrix instructions of tile A / B
-//   19        walks the block's items and publishes them to the others
+//   24        bulk copies of the halves (keys, values) of page records
+//   25, 26    issue the matrix instructions of tile A / B
+//   27        walks the block's items and publishes them to the others
 //
 // S = Q K^T comes from shared memory, O += P V takes P from tensor memory.  One
 // tile's softmax runs under the other's products, and so does the time from a
 // barrier to the first instruction after it (about 450 cycles; with one warp
 // issuing for both tiles it came four times per tile of keys and left the
 // tensor cores idle half the time: 1.22 ms against 0.XX).  S and O fill tensor
-// memory: 2 x 128 + 2 x D columns; P lies in the second half of its S.
+// memory: 2 x 128 + 2 x D columns; P lies over its S, each half row over its own.
 //
 // The running maximum is moved only when a row's grows by more than 2^kSlack:
 // until then O needs no rescaling, and P keeps fp16's relative precision.
@@ -32,10 +32,10 @@ namespace {
 
 constexpr int kRows = kRowsTile;
 constexpr int kKeys = 128;
-constexpr int kThreads = 640;  // at 96 registers; shared out as 256 x 136, 256 x 72, 128 x 64
+constexpr int kThreads = 896;  // at 72 registers; shared out as 512 x 88, 256 x 56, 128 x 40
 constexpr int kMaxSlots = 16;
-constexpr int kExpandV = 12, kLoad = 16, kMma = 17, kWalk = 19;
-constexpr int kReaders = 8 + 8 + 3;
+constexpr int kSoftmax = 16, kExpandV = 20, kLoad = 24, kMma = 25, kWalk = 27;
+constexpr int kReaders = 16 + 8 + 3;
 
 template <int D>
 struct Cfg {
@@ -43,8 +43,9 @@ struct Cfg {
   static constexpr int K_BYTES = kKeys * D * 2;   // one tile of keys; V the same
   static constexpr int SUB_Q = 128 * 128;         // 64-wide sub-tile of Q or K
   static constexpr int SUB_V = D * 128;           // 64-key sub-tile of V transposed
-  static constexpr int RING = D == 128 ? 33 * 1024 : 48 * 1024;
-  static constexpr int RING0 = 2 * Q_BYTES + 4 * K_BYTES;
+  static constexpr int BARS0 = 2 * Q_BYTES + 4 * K_BYTES;
+  static constexpr int RING0 = BARS0 + 3072;
+  static constexpr int RING = (D == 128 ? 227 : 160) * 1024 - RING0;
 };
 
 struct Bars {
@@ -52,9 +53,11 @@ struct Bars {
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t qfull[2], sfull[2], pfull[2], ofull[2], turn[2], done;
   ItemRing items;
+  float swap[2][2][128];  // between the two threads of a row: [tile][half][row]
   uint32_t tmem;
   int abort;
 };
+static_assert(sizeof(Bars) <= 3072, "between the operand tiles and the ring");
 
 // D[tmem] (+)= A[smem] * B[smem]^T from a whole converged warp.
 DEVINL void umma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -71,10 +74,10 @@ DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
-// One query row (thread's) to fp16 in the swizzled tile; returns the softmax
-// scale of the row in log2 units (> 0).
+// Half h of a query row to fp16 in the swizzled tile; returns the softmax scale
+// of the row in log2 units (> 0).
 template <int D>
-DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, uint32_t tile) {
+DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, int h, uint32_t tile) {
   const bool have = idx < t.nq * p.G;
   const int tok = idx / p.G;
   const uint4* src = reinterpret_cast<const uint4*>(p.q + (t.q0 + tok) * p.q_stride + (t.h * p.G + idx - tok * p.G) * D);
@@ -91,7 +94,7 @@ DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, uint32_t
   float up, sc;
   row_scale(p.scale * __ldg(p.g_k + t.h), top, up, sc);
 #pragma unroll 2
-  for (int i = 0; i < D / 8; ++i) {
+  for (int i = h * (D / 16); i < (h + 1) * (D / 16); ++i) {
     uint4 v = make_uint4(0, 0, 0, 0);
     if (have) v = __ldg(src + i);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -107,12 +110,12 @@ DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, uint32_t
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParams p, int slots) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ Bars bars;
-  // 1024-byte aligned operand tiles: Q_A Q_B | K0 K1 | V0 V1 | ring of record halves
-  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
-  const uint32_t sq = base, sk = base + 2 * C::Q_BYTES, sv = sk + 2 * C::K_BYTES, ring_s = base + C::RING0;
-  uint8_t* ring = smem_raw + (ring_s - raw);
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // 1024-byte aligned operand tiles: Q_A Q_B | K0 K1 | V0 V1 | barriers | ring of record halves
+  const uint32_t base = smem_u32(smem_raw);
+  const uint32_t sq = base, sk = base + 2 * C::Q_BYTES, sv = sk + 2 * C::K_BYTES;
+  Bars& bars = *reinterpret_cast<Bars*>(smem_raw + C::BARS0);
+  uint8_t* ring = smem_raw + C::RING0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = record_bytes(p.P, D) / 2, pages = kKeys / p.P;
   const unsigned long long tmo = p.timeout_ns;
@@ -127,9 +130,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       mbar_init(&bars.kempty[i], 2);
       mbar_init(&bars.vfull[i], 4);
       mbar_init(&bars.vempty[i], 2);
-      mbar_init(&bars.qfull[i], 4);
+      mbar_init(&bars.qfull[i], 8);
       mbar_init(&bars.sfull[i], 1);
-      mbar_init(&bars.pfull[i], 4);
+      mbar_init(&bars.pfull[i], 8);
       mbar_init(&bars.ofull[i], 1);
       mbar_init(&bars.turn[i], 1);
     }
@@ -151,50 +154,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
   const long long x0 = blockIdx.x * range, x1 = min(total, x0 + range);
   int* const abort = &bars.abort;
   if (x0 < x1) {
-    if (warp < 8) {
+    if (warp < kSoftmax) {
       // ================================================================ softmax
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
-      const int g = warp >> 2;                       // tile A or B
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
+      const int g = warp >> 3, h = (warp >> 2) & 1;  // tile A or B; keys 64 h .. of S, columns h D/2 .. of O
       const int r = (warp & 3) * 32 + lane;          // row in the tile
+      const int pair_bar = 1 + 4 * g + (warp & 3);   // of the two warps that share 32 rows
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t ts = tmem + lanes + g * 128, to = tmem + lanes + 256 + g * 128;
-      const uint32_t tile_q = sq + g * C::Q_BYTES;
+      const uint32_t ts = tmem + lanes + g * 128 + 64 * h, to = tmem + lanes + 256 + g * 128 + h * (D / 2);
+      float* const give = &bars.swap[g][h][r];
+      const float* const take = &bars.swap[g][h ^ 1][r];
       uint32_t cnt = 0;  // tiles of keys done
       ItemReader items;
       Item it, nx = items.next(bars.items, tmo, p.err, abort);
+      bool end = named_bar_red_or(pair_bar, 64, nx.n == 0);  // both warps leave together
       bool done_one = false;          // `it` holds an item whose output is still in tensor memory
       float sc = 0.0f;
       float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units); P's shift less it (0 for none)
-      uint64_t l2[2] = {0ull, 0ull};
+      uint64_t l2 = 0ull;
       while (true) {
         // the next item's queries while the last products of this one run
-        const bool mine = nx.n > 0 && nx.rows > g * 128;
+        const bool mine = !end && nx.rows > g * 128;
         float sc_next = 0.0f;
         if (mine) {
-          sc_next = load_q<D>(p, nx, nx.row0 + g * 128 + r, r, tile_q);
+          sc_next = load_q<D>(p, nx, nx.row0 + g * 128 + r, r, h, sq + g * C::Q_BYTES);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.qfull[g]);
         }
         if (done_one) {
           const int rr = g * 128 + r, idx = it.row0 + rr;
+          float l, lb;
+          unpair(l2, l, lb);
+          l += lb;
+          *give = l;
           wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
           tc_fence_after();
-          float l, lb;
-          unpair(add2(l2[0], l2[1]), l, lb);
-          l += lb;
+          named_bar_sync(pair_bar, 64);
+          l = h ? *take + l : l + *take;
           const int tok = idx / p.G;
           const long long row = static_cast<long long>(it.q0 + tok) * p.Hq + it.h * p.G + (idx - tok * p.G);
           const bool whole = it.slot < 0, have = rr < it.rows;
           const float inv = l > 0.0f ? __ldg(p.g_v + it.h) / l : 0.0f;
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
+          for (int q = 0; q < D / 64; ++q) {
             uint32_t o[32];
             tmem_ld_32x32b_x32(to + 32 * q, o);
             tmem_ld_wait();
             if (whole) {
               if (have) {
-                uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + 32 * q);
+                uint4* dst = reinterpret_cast<uint4*>(p.out + row * D + h * (D / 2) + 32 * q);
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                   uint32_t w[4];
@@ -205,41 +214,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 }
               }
             } else {
-              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (static_cast<long long>(it.slot) * kRows + rr) * D + 32 * q);
+              uint4* dst = reinterpret_cast<uint4*>(p.part_o + (static_cast<long long>(it.slot) * kRows + rr) * D +
+                                                    h * (D / 2) + 32 * q);
 #pragma unroll
               for (int v = 0; v < 8; ++v) dst[v] = make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
             }
           }
-          if (!whole) {
-            p.part_ml[static_cast<long long>(it.slot) * 2 * kRows + rr] = m;
-            p.part_ml[(static_cast<long long>(it.slot) * 2 + 1) * kRows + rr] = l;
-          } else if (p.lse && have) {
-            p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+          if (h == 0) {
+            if (!whole) {
+              p.part_ml[static_cast<long long>(it.slot) * 2 * kRows + rr] = m;
+              p.part_ml[(static_cast<long long>(it.slot) * 2 + 1) * kRows + rr] = l;
+            } else if (p.lse && have) {
+              p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+            }
           }
           tc_fence_before();
         }
-        if (nx.n == 0) break;
+        if (end) break;
         it = nx;
         done_one = mine;
         if (mine) {
           sc = sc_next;
-          const int idx = it.row0 + g * 128 + r;
           int lo = 0, hi = it.len;  // a row that is not there masks nothing
-          if (g * 128 + r < it.rows) item_keys(p, it, idx, lo, hi);
+          if (g * 128 + r < it.rows) item_keys(p, it, it.row0 + g * 128 + r, lo, hi);
+          lo -= it.u * kKeys + 64 * h;  // in the thread's 64 keys of the first tile
+          hi -= it.u * kKeys + 64 * h;
           m = -INFINITY, nb = 0.0f;
-          l2[0] = l2[1] = 0ull;
-          for (int i = 0; i < it.n; ++i, ++cnt) {
+          l2 = 0ull;
+          for (int i = 0; i < it.n; ++i, ++cnt, lo -= kKeys, hi -= kKeys) {
             wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, abort);
             tc_fence_after();
-            const int a = lo - (it.u + i) * kKeys, b = hi - (it.u + i) * kKeys;  // the row's keys, in the tile
-            if (!__all_sync(0xFFFFFFFFu, a <= 0 && b >= kKeys)) {  // some row does not see all of these keys
+            if (!__all_sync(0xFFFFFFFFu, lo <= 0 && hi >= 64)) {  // some row does not see all of these keys
 #pragma unroll 1
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 2; ++q) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(ts + 32 * q, v);
                 tmem_ld_wait();
                 // bit j: key 32 q + j is seen
-                const int x = min(max(a - 32 * q, 0), 32), y = min(max(b - 32 * q, 0), 32);
+                const int x = min(max(lo - 32 * q, 0), 32), y = min(max(hi - 32 * q, 0), 32);
                 const uint32_t see = static_cast<uint32_t>(((1ull << y) - 1ull) & ~((1ull << x) - 1ull));
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -248,79 +260,61 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               }
               tmem_st_wait();
             }
-            auto largest = [&](const uint32_t (&v)[32], float x) {
-              float y = __uint_as_float(v[0]);
-#pragma unroll
-              for (int j = 1; j < 29; j += 4) {
-                x = fmaxf(fmaxf(x, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
-                y = fmaxf(fmaxf(y, __uint_as_float(v[j + 2])), __uint_as_float(v[j + 3]));
-              }
-              x = fmaxf(fmaxf(x, __uint_as_float(v[29])), __uint_as_float(v[30]));
-              return fmaxf(fmaxf(x, y), __uint_as_float(v[31]));
-            };
-            // S is read twice, 32 keys at a time, the next ones on their way
             uint32_t va[32], vb[32];
-            float top = -INFINITY;
             tmem_ld_32x32b_x32(ts, va);
-#pragma unroll 1
-            for (int q = 0; q < 4; q += 2) {
-              tmem_ld_wait();
-              tmem_ld_32x32b_x32(ts + 32 * (q + 1), vb);
-              top = largest(va, top);
-              tmem_ld_wait();
-              tmem_ld_32x32b_x32(ts + 32 * (q ? 3 : 2), va);  // the second time round: keys 96 .. 127 again
-              top = largest(vb, top);
+            tmem_ld_32x32b_x32(ts + 32, vb);
+            tmem_ld_wait();
+            float top = __uint_as_float(va[0]), alt = __uint_as_float(vb[0]);
+#pragma unroll
+            for (int j = 1; j < 31; j += 2) {
+              top = fmaxf(fmaxf(top, __uint_as_float(va[j])), __uint_as_float(va[j + 1]));
+              alt = fmaxf(fmaxf(alt, __uint_as_float(vb[j])), __uint_as_float(vb[j + 1]));
             }
-            top *= sc;
-            const bool grow = top > m + kSlack;  // also the row's first keys
-            if (__any_sync(0xFFFFFFFFu, grow)) {
+            top = fmaxf(fmaxf(top, __uint_as_float(va[31])), fmaxf(alt, __uint_as_float(vb[31]))) * sc;
+            // does any row of the pair's 32 need a new maximum? (also the rows' first keys)
+            if (named_bar_red_or(pair_bar, 64, top > m + kSlack)) {
+              *give = top;
+              named_bar_sync(pair_bar, 64);
+              top = fmaxf(top, *take);
               float f = 1.0f;
-              if (grow) {
+              if (top > m + kSlack) {
                 f = m == -INFINITY ? 0.0f : ex2(m - top);
                 m = top;
                 nb = kShift - top;
               }
-              const uint64_t ff = pair(f, f);
-#pragma unroll
-              for (int q = 0; q < 2; ++q) l2[q] = fma2(l2[q], ff, 0ull);
+              l2 = fma2(l2, pair(f, f), 0ull);
               if (i > 0) {  // O holds something: bring it to the new maximum
                 wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
-                  uint32_t o[16];
-                  tmem_ld_32x32b_x16(to + 16 * q, o);
+                  uint32_t o[8];
+                  tmem_ld_32x32b_x8(to + 8 * q, o);
                   tmem_ld_wait();
 #pragma unroll
-                  for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                  tmem_st_32x32b_x16(to + 16 * q, o);
+                  for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                  tmem_st_32x32b_x8(to + 8 * q, o);
                 }
               }
             }
             const uint64_t sc2 = pair(sc, sc), nb2 = pair(nb, nb);
-            auto weigh = [&](int q, const uint32_t (&v)[32]) {  // P of 32 keys
-              uint32_t w[16];
+            auto weigh = [&](int q, const uint32_t* v) {  // P of 16 keys, over the thread's own columns
+              uint32_t w[8];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 float x, y;
                 unpair(fma2(pair(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), sc2, nb2), x, y);
                 x = ex2(x);
                 y = ex2(y);
-                l2[j & 1] = add2(l2[j & 1], pair(x, y));
+                l2 = add2(l2, pair(x, y));
                 w[j] = pack_f16x2(x, y);
               }
-              tmem_st_32x32b_x16(ts + 64 + 16 * q, w);
+              tmem_st_32x32b_x8(ts + 8 * q, w);
             };
-            // from the last keys on: P's columns lie over keys already taken
-#pragma unroll 1
-            for (int q = 3; q > 0; q -= 2) {
-              tmem_ld_wait();
-              tmem_ld_32x32b_x32(ts + 32 * (q - 1), vb);
-              weigh(q, va);
-              tmem_ld_wait();
-              if (q > 1) tmem_ld_32x32b_x32(ts + 32 * (q - 2), va);
-              weigh(q - 1, vb);
-            }
+            weigh(0, va);
+            weigh(1, va + 16);
+            weigh(2, vb);
+            weigh(3, vb + 16);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -328,11 +322,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           }
         }
         nx = items.next(bars.items, tmo, p.err, abort);
+        end = named_bar_red_or(pair_bar, 64, nx.n == 0);
       }
     } else {
       if (warp < kLoad) {
         // ============================================================== expand
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const bool is_v = warp >= kExpandV;
         const int w = warp & 3, c4 = lane & 3;
         const int tg = lane & 7, tgh = w & 1;  // V: group of 8 keys in a 64-key sub-tile
@@ -428,24 +423,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               for (int q = 0; q < 4; ++q) f[q] = e4m3x2_to_f16x2(sb[2 * q] | (sb[2 * q + 1] << 8));
               const uint32_t vt = sv + st * C::K_BYTES + tgh * C::SUB_V + 16 * blk * 128;
 #pragma unroll
-              for (int v = 0; v < 2; ++v) {
-                uint32_t h[8][4];
+              for (int v = 0; v < 4; ++v) {  // word v / 2, even or odd values
+                uint32_t h[4][4];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                  const uint32_t x = v ? cw[2 * q].y : cw[2 * q].x, y = v ? cw[2 * q + 1].y : cw[2 * q + 1].x;
+                  const uint32_t x = v >> 1 ? cw[2 * q].y : cw[2 * q].x, y = v >> 1 ? cw[2 * q + 1].y : cw[2 * q + 1].x;
                   const uint32_t a = odd ? y : x, b = odd ? x : y;
-                  uint32_t even[4], odds[4];
-                  e2m1x8((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), even);
-                  e2m1x8(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), odds);
+                  uint32_t e[4];
+                  e2m1x8(v & 1 ? ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u)
+                               : (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), e);
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    h[2 * k][q] = hmul2(even[k], f[q]);
-                    h[2 * k + 1][q] = hmul2(odds[k], f[q]);
-                  }
+                  for (int k = 0; k < 4; ++k) h[k][q] = hmul2(e[k], f[q]);
                 }
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                  st_shared_v4(vt + (8 * v + k) * 128 + ((tg ^ k) << 4), h[k][0], h[k][1], h[k][2], h[k][3]);
+                for (int k = 0; k < 4; ++k) {
+                  const int d = 2 * k + (v & 1);  // in the word
+                  st_shared_v4(vt + (8 * (v >> 1) + d) * 128 + ((tg ^ d) << 4), h[k][0], h[k][1], h[k][2], h[k][3]);
+                }
               }
             }
             fence_proxy_async_smem();
@@ -458,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           }
         }
       } else {
-       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+       asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
        if (warp == kLoad) {
         // ================================================================ load
         // Lane l feeds slot l, each at its own pace: one thread for all slots
@@ -553,24 +547,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           const bool more = rem > 0, mine = more && nx.rows > g * 128;
           if (more) wait_warp(&bars.kfull[st], (j >> 1) & 1, tmo, p.err, abort);
           if (cur) wait_warp(&bars.vfull[so], ((j - 1) >> 1) & 1, tmo, p.err, abort);
-          if (cur_mine) {
-            wait_warp(&bars.pfull[g], pp, tmo, p.err, abort);
-            pp ^= 1;
-          }
-          if (mine && nx_first) {
-            wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
-            pq ^= 1;
-          }
           // The tiles take turns, each after the other's products are done: left
           // to themselves they fall into step, and the tensor cores idle while
           // both are in their softmax.
           if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, tmo, p.err, abort);
+          if (mine && nx_first) {
+            wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
+            pq ^= 1;
+          }
+          if (cur_mine) {
+            wait_warp(&bars.pfull[g], pp, tmo, p.err, abort);
+            pp ^= 1;
+          }
           tc_fence_after();
           if (cur_mine) {
             const uint64_t b = dv + so * (C::K_BYTES >> 4);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_f16_ts_warp(to, ts + 64 + 8 * kk, b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
+              umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
                                cur_first && kk == 0 ? 0u : 1u);
             umma_commit_warp(&bars.ofull[g]);
             umma_commit_warp(&bars.vempty[so]);
@@ -617,13 +611,13 @@ int launch(const AttnParams& p, cudaStream_t s) {
   using C = Cfg<D>;
   const int half = record_bytes(p.P, D) / 2;
   const int slots = std::min(kMaxSlots, C::RING / half);
-  const int smem = 1024 + C::RING0 + slots * half;
+  const int smem = C::RING0 + slots * half;
   static bool set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!set[dev]) {
     const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               1024 + C::RING0 + C::RING);
+                                               C::RING0 + C::RING);
     if (e != cudaSuccess) {
       set_cuda_error(e);
       return MOE_ERR_CUDA;
