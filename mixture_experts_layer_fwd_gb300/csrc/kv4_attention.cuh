@@ -254,14 +254,15 @@ DEVINL void item_keys(const AttnParams& p, const Item& t, int idx, int& lo, int&
 }
 
 // Bounded wait of a whole warp, every lane testing: mbar_wait_bounded's rules.
-// The test suspends the warp in hardware for a while by itself (a given
-// suspend time makes it sleep in steps that cost a round trip each: measured
-// 1.33 against 1.22 ms on a 4096-token chunk at 12289 keys); the clock is
-// read once in 64 tests.
+// The test suspends the warp in hardware for a few tens of cycles by itself
+// (given a suspend time it sleeps in steps that cost a round trip each); the
+// clock is read once in 64 tests.  LAZY: for warps that nothing waits for soon.
+template <bool LAZY = false>
 DEVINL void wait_warp(uint64_t* bar, uint32_t parity, unsigned long long tmo, unsigned int* err, volatile int* abort) {
   if (!mbar_try_wait(bar, parity)) {
     uint64_t t0 = 0;
     for (uint32_t k = 1; !mbar_try_wait(bar, parity); ++k) {
+      if (LAZY) __nanosleep(200);
       if (k & 63u) continue;
       const uint64_t now = globaltimer_ns();
       if (t0 == 0) t0 = now;
@@ -293,7 +294,7 @@ struct ItemWriter {
   int i = 0;
   DEVINL void put(ItemRing& r, const Item& t, unsigned long long tmo, unsigned int* err, volatile int* abort) {
     const int k = i & (kItems - 1);
-    if (i >= kItems) wait_warp(&r.empty[k], (i / kItems - 1) & 1, tmo, err, abort);
+    if (i >= kItems) wait_warp<true>(&r.empty[k], (i / kItems - 1) & 1, tmo, err, abort);
     if ((threadIdx.x & 31) == 0) {
       r.item[k] = t;
       mbar_arrive(&r.full[k]);

@@ -162,12 +162,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       const int pair_bar = 1 + 4 * g + (warp & 3);   // of the two warps that share 32 rows
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + g * 128 + 64 * h, to = tmem + lanes + 256 + g * 128 + h * (D / 2);
+      // One warp of the tile's eight tests a barrier, the others wait for it at a
+      // hardware barrier: eight warps testing took half the issue slots.
+      const int tile_bar = 9 + g;
+      const bool tests = (warp & 7) == 0;
       float* const give = &bars.swap[g][h][r];
       const float* const take = &bars.swap[g][h ^ 1][r];
       uint32_t cnt = 0;  // tiles of keys done
       ItemReader items;
       Item it, nx = items.next(bars.items, tmo, p.err, abort);
-      bool end = named_bar_red_or(pair_bar, 64, nx.n == 0);  // both warps leave together
+      bool end = named_bar_red_or(tile_bar, 256, nx.n == 0);  // all eight leave together
       bool done_one = false;          // `it` holds an item whose output is still in tensor memory
       float sc = 0.0f;
       float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units); P's shift less it (0 for none)
@@ -188,9 +192,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           unpair(l2, l, lb);
           l += lb;
           *give = l;
-          wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
+          if (tests) wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
+          named_bar_sync(tile_bar, 256);
           tc_fence_after();
-          named_bar_sync(pair_bar, 64);
           l = h ? *take + l : l + *take;
           const int tok = idx / p.G;
           const long long row = static_cast<long long>(it.q0 + tok) * p.Hq + it.h * p.G + (idx - tok * p.G);
@@ -242,7 +246,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           m = -INFINITY, nb = 0.0f;
           l2 = 0ull;
           for (int i = 0; i < it.n; ++i, ++cnt, lo -= kKeys, hi -= kKeys) {
-            wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, abort);
+            if (tests) wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, abort);
+            named_bar_sync(tile_bar, 256);
             tc_fence_after();
             if (!__all_sync(0xFFFFFFFFu, lo <= 0 && hi >= 64)) {  // some row does not see all of these keys
 #pragma unroll 1
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           }
         }
         nx = items.next(bars.items, tmo, p.err, abort);
-        end = named_bar_red_or(pair_bar, 64, nx.n == 0);
+        end = named_bar_red_or(tile_bar, 256, nx.n == 0);
       }
     } else {
       if (warp < kLoad) {
@@ -330,6 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         const bool is_v = warp >= kExpandV;
         const int w = warp & 3, c4 = lane & 3;
+        const int team_bar = is_v ? 12 : 11;  // warp 0 tests barriers for the four
         const int tg = lane & 7, tgh = w & 1;  // V: group of 8 keys in a 64-key sub-tile
         const int blk = D == 128 ? (2 * (tg >> 1) + (lane >> 3) + 4 * (w >> 1)) & 7 : (2 * (tg >> 1) + (lane >> 3)) & 3;
         const int odd = tg & 1;
@@ -346,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         uint32_t j = 0;
         while (true) {
           const Item it = items.next(bars.items, tmo, p.err, abort);
-          if (it.n == 0) break;
+          if (named_bar_red_or(team_bar, 128, it.n == 0)) break;  // all four together
           for (int i = 0; i < it.n; ++i, ++j) {
             const uint32_t st = j & 1, ph = (j >> 1) & 1;
-            {
+            if (w == 0) {
               int sl = slot;
               uint32_t rd = round;
               for (int pg = 0; pg < pages; ++pg) {
@@ -357,7 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 if (++sl == slots) sl = 0, rd ^= 1;
               }
             }
-            if (j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, tmo, p.err, abort);
+            if (w == 0 && j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, tmo, p.err, abort);
+            named_bar_sync(team_bar, 128);
             if (!is_v) {
               // lane = (key, quarter of its values); the warp's keys are 32k + 8w ..
               constexpr int W = D / 32;  // words of 8 codes per lane
@@ -471,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           int k = lane < slots ? (lane >= at ? lane - at : lane - at + slots) : all;
           int id = -2;  // page of half k: -2 not looked up, -1 none
           uint64_t t0 = 0;
-          for (uint32_t spin = 1; __any_sync(0xFFFFFFFFu, k < all); ++spin) {
+          while (__any_sync(0xFFFFFFFFu, k < all)) {
+            bool moved = false;
             if (k < all) {
               const int in = k & (2 * pages - 1);
               if (id == -2) {
@@ -495,19 +503,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 ++uses;
                 k += slots;
                 id = -2;
+                moved = true;
               }
             }
-            if ((spin & 255u) == 0u) {
+            if (__any_sync(0xFFFFFFFFu, moved)) {
+              t0 = 0;
+            } else {
               const uint64_t now = globaltimer_ns();
               if (t0 == 0) t0 = now;
-              const bool late = now - t0 > tmo && k < all && uses > 0 && !mbar_test_wait(&bars.empty[lane], (uses - 1) & 1);
-              if (__any_sync(0xFFFFFFFFu, late)) {
+              if (now - t0 > tmo) {
                 atomicOr(p.err, kErrTimeout);
                 *static_cast<volatile int*>(abort) = 1;
               }
               if (*static_cast<volatile int*>(abort)) break;
-            } else if (spin & 1u) {
-              t0 = __any_sync(0xFFFFFFFFu, id == -2) ? 0 : t0;  // something moved
+              __nanosleep(100);
             }
           }
           at = (at + all) % slots;
@@ -547,9 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           const bool more = rem > 0, mine = more && nx.rows > g * 128;
           if (more) wait_warp(&bars.kfull[st], (j >> 1) & 1, tmo, p.err, abort);
           if (cur) wait_warp(&bars.vfull[so], ((j - 1) >> 1) & 1, tmo, p.err, abort);
-          // The tiles take turns, each after the other's products are done: left
-          // to themselves they fall into step, and the tensor cores idle while
-          // both are in their softmax.
+          // The tiles take turns, one's products queued while the other's S is in
+          // the making: left to themselves they fall into step, and the tensor
+          // cores idle while both are in their softmax.
           if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, tmo, p.err, abort);
           if (mine && nx_first) {
             wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
@@ -567,6 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
                                cur_first && kk == 0 ? 0u : 1u);
             umma_commit_warp(&bars.ofull[g]);
+            umma_commit_warp(&bars.turn[g ^ 1]);
             umma_commit_warp(&bars.vempty[so]);
           } else if (cur && lane == 0) {
             mbar_arrive(&bars.vempty[so]);
@@ -583,8 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           } else if (more && lane == 0) {
             mbar_arrive(&bars.kempty[st]);
           }
-          if (cur_mine || mine) umma_commit_warp(&bars.turn[g ^ 1]);
-          else if (lane == 0) mbar_arrive(&bars.turn[g ^ 1]);
+          if (!cur_mine && lane == 0) mbar_arrive(&bars.turn[g ^ 1]);
           __syncwarp();
           cur = more, cur_mine = mine, cur_first = nx_first;
           nx_first = false;
