@@ -35,6 +35,7 @@ constexpr int kSmem = 226 * 1024;
 template <int ROWS>
 __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int unit) {
   __shared__ long long s_warp[32];
+  launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto scan = [&](long long v, long long& total) {
     long long incl = v;
@@ -114,46 +115,96 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int
 }
 
 // -------------------------------------------------------------------- joining
-// Block (c, y): the item that is cut first at the start of range c; the rows
-// y, y + gridDim.y, ... of it, one warp each.
-template <int ROWS, int D>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p, int unit) {
-  const long long total = total_units(p), range = range_of(p, total);
-  const int c = blockIdx.x + 1;
-  const long long cut = c * range;
-  if (cut >= total) return;
-  const Cursor cur = cursor_at<ROWS>(p, unit, cut);
-  const long long start = cut - (cur.u - cur.u0);
-  if (start == cut || start < cut - range) return;  // not cut here, or first cut at an earlier range
-  const long long end = start + (cur.u1 - cur.u0);
-  const int last = static_cast<int>((end - 1) / range);
+// Block (c, y): the item whose first part lies in range c; WARPS warps per row
+// share its parts, rows y * RPB .. of the item.  Parts are added in a fixed
+// order, first those of one warp, then the warps'.
+template <int ROWS, int D, int WARPS>
+__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
+  constexpr int RPB = 4 / WARPS;  // rows per block at a time
+  constexpr int V = D / 32;       // columns per lane
+  __shared__ float s_o[4][D], s_l[4], s_m[4];
+  wait_for_previous();
+  const int c = blockIdx.x;
+  const PartItem* notes = reinterpret_cast<const PartItem*>(p.part_item);
+  const PartItem t = notes[2 * c + 1];
+  if (t.rows == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rows = min(ROWS, cur.s.n * p.G - cur.tile * ROWS);
-  for (int r = blockIdx.y * 4 + warp; r < rows; r += gridDim.y * 4) {
-    float m = -INFINITY;
-    for (int i = c - 1; i <= last; ++i) m = fmaxf(m, p.part_ml[(2 * i + (i == c - 1)) * 2 * ROWS + r]);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[D / 32];
+  const int w = warp % WARPS, sub = warp / WARPS;
+  for (int r0 = blockIdx.y * RPB; r0 < t.rows; r0 += gridDim.y * RPB) {
+    const int r = r0 + sub;
+    const bool have = r < t.rows;
+    float m = -INFINITY, l = 0.0f, o[V];
 #pragma unroll
-    for (int v = 0; v < D / 32; ++v) o[v] = 0.0f;
-    for (int i = c - 1; i <= last; ++i) {
-      const int slot = 2 * i + (i == c - 1);
-      const float f = exp2f(p.part_ml[slot * 2 * ROWS + r] - base);
-      l += f * p.part_ml[(slot * 2 + 1) * ROWS + r];
-      const float* po = p.part_o + (static_cast<long long>(slot) * ROWS + r) * D + lane * (D / 32);
+    for (int v = 0; v < V; ++v) o[v] = 0.0f;
+    if (have) {
+      // lane j looks at parts c + w + WARPS * j, 32 at a time
+      for (int base = c + w; base <= t.last; base += 32 * WARPS) {
+        const int mine = base + WARPS * lane;
+        const long long slot = 2ll * mine + (mine == c);
+        float pm = -INFINITY, pl = 0.0f;
+        if (mine <= t.last) {
+          pm = p.part_ml[slot * 2 * ROWS + r];
+          pl = p.part_ml[(slot * 2 + 1) * ROWS + r];
+        }
+        float top = pm;
 #pragma unroll
-      for (int v = 0; v < D / 32; ++v) o[v] += f * po[v];
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        const float mn = fmaxf(m, top);
+        const float ref = mn == -INFINITY ? 0.0f : mn;
+        const float old = ex2(m - ref);
+        const float f = ex2(pm - ref);
+        float sum = f * pl;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+        l = l * old + sum;
+        m = mn;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] *= old;
+        const int n = min(32, (t.last - base) / WARPS + 1);
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) {
+          const int i = base + WARPS * j;
+          const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
+          const float* po = p.part_o + ((2ll * i + (i == c)) * ROWS + r) * D + lane * V;
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += fj * po[v];
+        }
+      }
     }
-    const int idx = cur.tile * ROWS + r;
-    const long long row = static_cast<long long>(cur.s.q0 + idx / p.G) * p.Hq + cur.h * p.G + idx % p.G;
-    const float inv = l > 0.0f ? __ldg(p.g_v + cur.h) / l : 0.0f;
-    uint32_t w[D / 64];
+    if (WARPS > 1) {
+      if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
-    for (int v = 0; v < D / 64; ++v) w[v] = pack_bf16x2(o[2 * v] * inv, o[2 * v + 1] * inv);
-    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (D / 64);
+      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = o[v];
+      __syncthreads();
+      if (w == 0 && have) {
+        float mx = m;
 #pragma unroll
-    for (int v = 0; v < D / 64; ++v) dst[v] = w[v];
-    if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+        for (int x = 1; x < WARPS; ++x) mx = fmaxf(mx, s_m[warp + x]);
+        const float ref = mx == -INFINITY ? 0.0f : mx;
+        const float f0 = ex2(m - ref);
+        l *= f0;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] *= f0;
+#pragma unroll
+        for (int x = 1; x < WARPS; ++x) {
+          const float f = ex2(s_m[warp + x] - ref);
+          l += f * s_l[warp + x];
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += f * s_o[warp + x][lane * V + v];
+        }
+        m = mx;
+      }
+      __syncthreads();
+    }
+    if (w == 0 && have) {
+      const int idx = t.row0 + r, tok = idx / p.G;
+      const long long row = static_cast<long long>(t.q0 + tok) * p.Hq + t.h * p.G + (idx - tok * p.G);
+      const float inv = l > 0.0f ? __ldg(p.g_v + t.h) / l : 0.0f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (V / 2);
+#pragma unroll
+      for (int v = 0; v < V / 2; ++v) dst[v] = pack_bf16x2(o[2 * v] * inv, o[2 * v + 1] * inv);
+      if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+    }
   }
 }
 
@@ -168,6 +219,7 @@ DEVINL void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
 template <int D>
 struct Group {
   uint64_t full[kMaxStages], empty[kMaxStages];
+  ItemRing items;
   float m[kWarps][kRows], l[kWarps][kRows];
   int abort;
   alignas(16) float o[kWarps][kRows][D / 2];  // half the columns at a time
@@ -193,91 +245,64 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
+    item_ring_init(sh.items, kWarps);
     sh.abort = 0;
     fence_mbar_init();
   }
   __syncthreads();
 
+  launch_dependents();
+  wait_for_previous();
   const int block = blockIdx.x * kGroups + grp;  // the group's range
   const long long total = total_units(p), range = range_of(p, total);
   const long long x0 = block * range, x1 = min(total, x0 + range);
+  int* const abort = &sh.abort;
 
   if (warp >= kGroups * kWarps) {
-    // -------- producers, one per group: one page record per stage
+    // -------- one warp per group walks its range and feeds its ring, a page record per stage
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (grp >= kGroups || x0 >= x1) return;
-    Cursor c = cursor_at<kRows>(p, p.P, x0);
-    uint32_t it = 0;
-    long long left = x1 - x0;
-    while (left > 0) {
-      const int n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
-      const int32_t* row = p.table + static_cast<long long>(c.b) * p.max_pages + c.u;
-      for (int base = 0; base < n; base += 32) {
-        const int at = base + lane;
-        int page = -1;
-        if (at < n && (c.u + at) * p.P < c.s.len) {
-          page = __ldg(row + at);
-          if (page < 0 || page >= p.num_pages) {
-            atomicOr(p.err, kErrBadIndex);
-            page = 0;
-          }
-        }
-        const int m = min(32, n - base);
-        for (int i = 0; i < m; ++i, ++it) {
-          const int pg = __shfl_sync(0xFFFFFFFFu, page, i);
-          const int st = it % stages;
-          if (lane == 0) {
-            if (it >= static_cast<uint32_t>(stages))
-              mbar_wait_bounded(&sh.empty[st], (it / stages - 1) & 1, p.timeout_ns, p.err, &sh.abort, true);
-            if (pg < 0 || *static_cast<volatile int*>(&sh.abort)) {
-              mbar_arrive(&sh.full[st]);  // no key in this unit
-            } else {
-              mbar_arrive_expect_tx(&sh.full[st], rec);
-              bulk_load(ring + static_cast<size_t>(st) * rec,
-                        p.pool + (static_cast<long long>(pg) * p.Hkv + c.h) * rec, rec, &sh.full[st]);
-            }
-          }
-          __syncwarp();
-        }
-      }
-      left -= n;
-      if (left > 0) cursor_next<kRows>(p, p.P, c);
-    }
-    // copies in flight are all waited for by the consumers, whose waits are
-    // bounded too; after a time-out this warp stays until they have landed
-    if (*static_cast<volatile int*>(&sh.abort) && lane == 0)
-      for (uint32_t k = it > static_cast<uint32_t>(stages) ? it - stages : 0; k < it; ++k)
-        mbar_wait_bounded(&sh.full[k % stages], (k / stages) & 1, p.timeout_ns, p.err, nullptr);
+    if (grp >= kGroups) return;
+    ItemWriter out;
+    Feeder feeder;
+    walk_range<kRows>(p, p.P, block, x0, x1, range, [&](const Item& t) {
+      out.put(sh.items, t, p.timeout_ns, p.err, abort);
+      if (t.n > 0)
+        feeder.feed(
+            p, t, t.n, rec, rec, [&](int k) { return t.u + k; }, [](int) { return 0; }, ring, sh.full, sh.empty, stages,
+            abort);
+      return *static_cast<volatile int*>(abort) == 0;
+    });
+    if (*static_cast<volatile int*>(abort)) feeder.drain(p, sh.full);
     return;
   }
 
   // -------- consumers: warp w of the group takes the stages w, w + 4, ...
   asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
-  if (x0 >= x1) return;
   const int wg = warp % kWarps;
   const int g = lane >> 2, c4 = lane & 3;
-  Cursor c = cursor_at<kRows>(p, p.P, x0);
+  ItemReader items;
   uint32_t it = 0;
-  long long left = x1 - x0;
-  while (left > 0) {
-    const int n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
+  while (true) {
+    const Item t = items.next(sh.items, p.timeout_ns, p.err, abort);
+    if (named_bar_red_or(1 + grp, 32 * kWarps, t.n == 0)) return;  // all four together
+    const int n = t.n;
     // rows g and g + 8 of the tile
     uint32_t qa[KS][4];
     float sc[2];
     int lo[2], hi[2];
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const int idx = c.tile * kRows + g + 8 * half;
-      const bool have = idx < c.s.n * p.G;
+      const int idx = t.row0 + g + 8 * half;
+      const bool have = g + 8 * half < t.rows;
       const int tok = idx / p.G;
-      lo[half] = 0, hi[half] = c.s.len;  // a row that is not there masks nothing
-      if (have) row_keys(p, c.s, tok, lo[half], hi[half]);
+      lo[half] = 0, hi[half] = t.len;  // a row that is not there masks nothing
+      if (have) item_keys(p, t, idx, lo[half], hi[half]);
       uint32_t w[LD / 2];
 #pragma unroll
       for (int i = 0; i < LD / 2; ++i) w[i] = 0;
       if (have) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (c.s.q0 + tok) * p.q_stride +
-                                                          (c.h * p.G + idx % p.G) * D + c4 * LD);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (t.q0 + tok) * p.q_stride +
+                                                          (t.h * p.G + idx - tok * p.G) * D + c4 * LD);
 #pragma unroll
         for (int i = 0; i < LD / 8; ++i) {
           const uint4 v = __ldg(src + i);
@@ -290,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
       top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
       float up;
-      row_scale(p.scale * __ldg(p.g_k + c.h), top, up, sc[half]);
+      row_scale(p.scale * __ldg(p.g_k + t.h), top, up, sc[half]);
 #pragma unroll
       for (int i = 0; i < LD / 2; ++i)
         qa[i >> 1][half + 2 * (i & 1)] =
@@ -311,20 +336,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
     for (int i = (wg - static_cast<int>(it)) & (kWarps - 1); i < n; i += kWarps) {
       const uint32_t at = it + i;
       const int st = at % stages;
-      mbar_wait_warp(&sh.full[st], (at / stages) & 1, p.timeout_ns, p.err, &sh.abort);
+      wait_warp(&sh.full[st], (at / stages) & 1, p.timeout_ns, p.err, abort);
       const uint8_t* kc = ring + static_cast<size_t>(st) * rec;
       const uint8_t* ks = kc + codes_bytes(p.P, D);
       const uint8_t* vc = kc + rec / 2;
       const uint8_t* vs = vc + codes_bytes(p.P, D);
-      const int key0 = (c.u + i) * p.P;
-      const int keys = min(p.P, c.s.len - key0);
+      const int key0 = (t.u + i) * p.P;
+      const int keys = min(p.P, t.len - key0);
 #pragma unroll 1
       for (int t0 = 0; t0 < keys; t0 += 32) {
         float s[4][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
-          const int tok = t0 + 8 * t + (g ^ ((g >> 1) & 1));
+        for (int kt = 0; kt < 4; ++kt) {
+          s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.0f;
+          const int tok = t0 + 8 * kt + (g ^ ((g >> 1) & 1));
           uint32_t w[LD / 8];
           uint32_t sb[2];
           if (LD == 32) {
@@ -346,18 +371,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
             const uint32_t f = sb[j >> 1];
 #pragma unroll
             for (int q = 0; q < 4; ++q) h[q] = hmul2(h[q], f);
-            mma_f16(s[t], qa[2 * j], h[0], h[1]);
-            mma_f16(s[t], qa[2 * j + 1], h[2], h[3]);
+            mma_f16(s[kt], qa[2 * j], h[0], h[1]);
+            mma_f16(s[kt], qa[2 * j + 1], h[2], h[3]);
           }
         }
         const int k0 = key0 + t0;
         if (k0 < all_lo || k0 + 32 > all_hi) {  // some row does not see all of these keys
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+          for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int key = k0 + 8 * t + ((2 * c4 + (q & 1)) ^ (c4 & 1));
-              if (key < lo[q >> 1] || key >= hi[q >> 1]) s[t][q] = -INFINITY;
+              const int key = k0 + 8 * kt + ((2 * c4 + (q & 1)) ^ (c4 & 1));
+              if (key < lo[q >> 1] || key >= hi[q >> 1]) s[kt][q] = -INFINITY;
             }
         }
         float top[2];
@@ -394,13 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
         for (int half = 0; half < 2; ++half) {
           const uint64_t sc2 = pair(sc[half], sc[half]), nb2 = pair(nb[half], nb[half]);
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
+          for (int kt = 0; kt < 4; ++kt) {
             float a, b;
-            unpair(fma2(pair(s[t][2 * half], s[t][2 * half + 1]), sc2, nb2), a, b);
+            unpair(fma2(pair(s[kt][2 * half], s[kt][2 * half + 1]), sc2, nb2), a, b);
             a = ex2(a);
             b = ex2(b);
             l2[half] = add2(l2[half], pair(a, b));
-            pa[t >> 1][2 * (t & 1) + half] = pack_f16x2(a, b);
+            pa[kt >> 1][2 * (kt & 1) + half] = pack_f16x2(a, b);
           }
         }
         const bool tail = t0 + 32 > keys;  // some of these keys were never written
@@ -449,9 +474,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
     it += n;
 
     // -------- the four warps' results become one, half the columns at a time
-    const bool whole = c.u == c.u0 && n == c.u1 - c.u0;
-    const int rows = min(kRows, c.s.n * p.G - c.tile * kRows);
-    const long long slot = 2ll * block + (c.u == c.u0 ? 1 : 0);
+    const bool whole = t.slot < 0;
+    const int rows = t.rows;
+    const long long slot = t.slot;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       float l, lb;
@@ -503,9 +528,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
           a.x += f * v.x, a.y += f * v.y, a.z += f * v.z, a.w += f * v.w;
         }
         if (whole) {
-          const int idx = c.tile * kRows + r;
-          const long long row = static_cast<long long>(c.s.q0 + idx / p.G) * p.Hq + c.h * p.G + idx % p.G;
-          const float inv = ll > 0.0f ? __ldg(p.g_v + c.h) / ll : 0.0f;
+          const int idx = t.row0 + r, tok = idx / p.G;
+          const long long row = static_cast<long long>(t.q0 + tok) * p.Hq + t.h * p.G + (idx - tok * p.G);
+          const float inv = ll > 0.0f ? __ldg(p.g_v + t.h) / ll : 0.0f;
           *reinterpret_cast<uint2*>(p.out + row * D + col) =
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
           if (p.lse && q == 0 && part == 0)
@@ -519,9 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
         }
       }
     }
-    named_bar_sync(1 + grp, 32 * kWarps);
-    left -= n;
-    if (left > 0) cursor_next<kRows>(p, p.P, c);
   }
 }
 
@@ -542,8 +564,7 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
     }
     set[dev] = true;
   }
-  attn_rows16_kernel<D><<<p.blocks / kGroups, kThreads, smem, s>>>(p, stages);
-  return check_launch();
+  return launch_after(attn_rows16_kernel<D>, dim3(p.blocks / kGroups), kThreads, smem, s, p, stages);
 }
 
 // Schedule, main kernel, joining.
@@ -552,11 +573,9 @@ int run(const AttnParams& p, int unit, cudaStream_t s) {
   attn_plan_kernel<ROWS><<<1, 1024, 0, s>>>(p, unit);
   MOE_TRY(check_launch());
   MOE_TRY(ROWS == kRows ? launch_rows16<D>(p, s) : attention_tiles(p, D, s));
-  if (p.blocks > 1) {
-    attn_join_kernel<ROWS, D><<<dim3(p.blocks - 1, ROWS == kRows ? 4 : 16), 128, 0, s>>>(p, unit);
-    MOE_TRY(check_launch());
-  }
-  return MOE_OK;
+  // few rows with many parts, or many rows with few
+  if (ROWS == kRows) return launch_after(attn_join_kernel<ROWS, D, 4>, dim3(p.blocks, 16), 128, 0, s, p);
+  return launch_after(attn_join_kernel<ROWS, D, 1>, dim3(p.blocks, 16), 128, 0, s, p);
 }
 
 constexpr int kTileRows = kRowsTile, kTileKeys = 128;
@@ -578,6 +597,7 @@ Layout layout(AttnParams& p, int D, void* ws) {
   p.starts = c.take<int>(p.B + 1);
   p.tile_base = c.take<int>(p.B + 1);
   p.unit_sum = c.take<long long>(tiles + 1);
+  p.part_item = c.take<int>(static_cast<size_t>(2) * r.blocks * 8);
   p.part_ml = c.take<float>(static_cast<size_t>(2) * r.blocks * 2 * r.rows);
   p.part_o = c.take<float>(static_cast<size_t>(2) * r.blocks * r.rows * D);
   p.blocks = r.blocks;

@@ -100,6 +100,7 @@ struct AttnParams {
   long long* unit_sum;  // [tiles + 1] units of one kv head before row tile f
   int blocks;           // ranges: blocks of the main kernel, or groups of its warps
   int min_units;        // least units of a block's range
+  int *part_item;  // [2 * blocks][8]: what a slot holds (PartItem)
   // partial results: slot 2 * block (the item begun by an earlier block) and 2 * block + 1
   float *part_o, *part_ml;  // [2 * blocks][ROWS][D], [2 * blocks][2][ROWS]
   unsigned int* err;
@@ -303,6 +304,138 @@ struct ItemWriter {
     ++i;
   }
 };
+
+// What a slot of the partial results holds; rows == 0: nothing.  The first
+// part of an item (an odd slot) also says which range holds its last part.
+struct PartItem {
+  int row0, rows, q0, h, last, pad[3];
+};
+static_assert(sizeof(PartItem) == 32, "eight words");
+
+// One lane's side of a ring of stages that bulk copies fill: lane l feeds slot
+// l, each at its own pace (one thread feeding all slots took about 900 cycles
+// per copy, in waits and barrier round trips).  An item's copies k = 0 .. all-1
+// take page_of(k) of its table row (one past the item's keys: nothing is
+// copied) from byte offset_of(k) of the record on.
+struct Feeder {
+  uint32_t uses = 0;  // of the lane's slot
+  int at = 0;         // slot of the item's first copy
+  template <class PageOf, class OffsetOf>
+  DEVINL void feed(const AttnParams& p, const Item& it, int all, int bytes, int rec, PageOf page_of,
+                   OffsetOf offset_of, uint8_t* ring, uint64_t* full, uint64_t* empty, int slots,
+                   volatile int* abort) {
+    const int lane = threadIdx.x & 31;
+    const uint8_t* pool = p.pool + static_cast<long long>(it.h) * rec;
+    const long long stride = static_cast<long long>(p.Hkv) * rec;
+    const int32_t* table = p.table + static_cast<long long>(it.b) * p.max_pages;
+    const int last = (it.len + p.P - 1) / p.P;
+    int k = lane < slots ? (lane >= at ? lane - at : lane - at + slots) : all;
+    int id = -2;  // page of copy k: -2 not looked up, -1 none
+    uint64_t t0 = 0;
+    while (__any_sync(0xFFFFFFFFu, k < all)) {
+      bool moved = false;
+      if (k < all) {
+        if (id == -2) {
+          const int pg = page_of(k);
+          id = -1;
+          if (pg < last) {
+            id = __ldg(table + pg);
+            if (id < 0 || id >= p.num_pages) {
+              atomicOr(p.err, kErrBadIndex);
+              id = 0;
+            }
+          }
+        }
+        if (uses == 0 || mbar_test_wait(&empty[lane], (uses - 1) & 1)) {
+          if (id < 0) {
+            mbar_arrive(&full[lane]);  // no key of this page
+          } else {
+            mbar_arrive_expect_tx(&full[lane], bytes);
+            bulk_load(ring + lane * bytes, pool + id * stride + offset_of(k), bytes, &full[lane]);
+          }
+          ++uses;
+          k += slots;
+          id = -2;
+          moved = true;
+        }
+      }
+      if (__any_sync(0xFFFFFFFFu, moved)) {
+        t0 = 0;
+      } else {
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > p.timeout_ns) {
+          atomicOr(p.err, kErrTimeout);
+          *abort = 1;
+        }
+        if (*abort) return;
+        __nanosleep(100);
+      }
+    }
+    at = (at + all) % slots;
+  }
+  // After a time-out elsewhere: stay until the copies in flight have landed.
+  DEVINL void drain(const AttnParams& p, uint64_t* full) {
+    if (uses > 0) mbar_wait_bounded(&full[threadIdx.x & 31], (uses - 1) & 1, p.timeout_ns, p.err, nullptr, true);
+  }
+};
+
+// Walks range `block` and hands its items to `use(item)`, the end mark (n == 0)
+// last; writes down what the range's two slots hold.  A whole warp calls it.
+template <int ROWS, class Use>
+DEVINL void walk_range(const AttnParams& p, int unit, int block, long long x0, long long x1, long long range, Use use) {
+  PartItem* notes = reinterpret_cast<PartItem*>(p.part_item) + 2 * block;
+  const bool writes = (threadIdx.x & 31) == 0;
+  bool noted[2] = {false, false};
+  if (x0 < x1) {
+    Cursor c = cursor_at<ROWS>(p, unit, x0);
+    long long x = x0;
+    while (true) {
+      const int n = static_cast<int>(min(x1 - x, static_cast<long long>(c.u1 - c.u)));
+      const Item t = make_item<ROWS>(p, c, n, block);
+      if (t.slot >= 0) {
+        const int side = t.slot & 1;
+        noted[side] = true;
+        if (writes) {
+          PartItem q;
+          q.row0 = t.row0, q.rows = t.rows, q.q0 = t.q0, q.h = t.h;
+          q.last = static_cast<int>((x + (c.u1 - c.u) - 1) / range);
+          notes[side] = q;
+        }
+      }
+      if (!use(t)) return;
+      x += n;
+      if (x >= x1) break;
+      cursor_next<ROWS>(p, unit, c);
+    }
+  }
+  if (writes) {
+    if (!noted[0]) notes[0].rows = 0;
+    if (!noted[1]) notes[1].rows = 0;
+  }
+  Item end{};
+  use(end);
+}
+
+// Programmatic dependent launch: the next kernel of the call may start its
+// prologue now; and: wait for the results of the one before.
+DEVINL void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... Params, class... Args>
+inline int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &a, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {
+    set_cuda_error(e);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
 
 DEVINL long long total_units(const AttnParams& p) { return p.unit_sum[p.tile_base[p.B]] * p.Hkv; }
 DEVINL long long range_of(const AttnParams& p, long long total) {

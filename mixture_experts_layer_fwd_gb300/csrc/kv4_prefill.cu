@@ -150,9 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
   tc_fence_after();
   const uint32_t tmem = bars.tmem;
 
+  launch_dependents();
+  wait_for_previous();
   const long long total = total_units(p), range = range_of(p, total);
   const long long x0 = blockIdx.x * range, x1 = min(total, x0 + range);
   int* const abort = &bars.abort;
+  if (x0 >= x1 && threadIdx.x < 2) reinterpret_cast<PartItem*>(p.part_item)[2 * blockIdx.x + threadIdx.x].rows = 0;
   if (x0 < x1) {
     if (warp < kSoftmax) {
       // ================================================================ softmax
@@ -462,81 +465,26 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
        if (warp == kLoad) {
         // ================================================================ load
-        // Lane l feeds slot l, each at its own pace: one thread for all slots
-        // took about 900 cycles per copy, in waits and barrier round trips.
-        uint32_t uses = 0;  // of the lane's slot
-        int at = 0;         // slot of the item's first half
+        Feeder feeder;
         ItemReader items;
+        const int shift = pages == 1 ? 1 : pages == 2 ? 2 : 3;  // halves of a tile: keys of its pages, then values
         while (true) {
           const Item it = items.next(bars.items, tmo, p.err, abort);
           if (it.n == 0) break;
-          const uint8_t* pool = p.pool + static_cast<long long>(it.h) * 2 * half;
-          const long long stride = static_cast<long long>(p.Hkv) * 2 * half;
-          const int32_t* table = p.table + static_cast<long long>(it.b) * p.max_pages;
-          const int first = it.u * pages, last = (it.len + p.P - 1) / p.P, all = 2 * pages * it.n;
-          const int shift = pages == 1 ? 1 : pages == 2 ? 2 : 3;  // halves of a tile: keys of its pages, then values
-          int k = lane < slots ? (lane >= at ? lane - at : lane - at + slots) : all;
-          int id = -2;  // page of half k: -2 not looked up, -1 none
-          uint64_t t0 = 0;
-          while (__any_sync(0xFFFFFFFFu, k < all)) {
-            bool moved = false;
-            if (k < all) {
-              const int in = k & (2 * pages - 1);
-              if (id == -2) {
-                const int pg = first + (k >> shift) * pages + (in & (pages - 1));
-                id = -1;
-                if (pg < last) {
-                  id = __ldg(table + pg);
-                  if (id < 0 || id >= p.num_pages) {
-                    atomicOr(p.err, kErrBadIndex);
-                    id = 0;
-                  }
-                }
-              }
-              if (uses == 0 || mbar_test_wait(&bars.empty[lane], (uses - 1) & 1)) {
-                if (id < 0) {
-                  mbar_arrive(&bars.full[lane]);  // no key of this page
-                } else {
-                  mbar_arrive_expect_tx(&bars.full[lane], half);
-                  bulk_load(ring + lane * half, pool + id * stride + (in < pages ? 0 : half), half, &bars.full[lane]);
-                }
-                ++uses;
-                k += slots;
-                id = -2;
-                moved = true;
-              }
-            }
-            if (__any_sync(0xFFFFFFFFu, moved)) {
-              t0 = 0;
-            } else {
-              const uint64_t now = globaltimer_ns();
-              if (t0 == 0) t0 = now;
-              if (now - t0 > tmo) {
-                atomicOr(p.err, kErrTimeout);
-                *static_cast<volatile int*>(abort) = 1;
-              }
-              if (*static_cast<volatile int*>(abort)) break;
-              __nanosleep(100);
-            }
-          }
-          at = (at + all) % slots;
+          feeder.feed(
+              p, it, 2 * pages * it.n, half, 2 * half,
+              [&](int k) { return it.u * pages + (k >> shift) * pages + (k & (pages - 1)); },
+              [&](int k) { return (k & pages) ? half : 0; }, ring, bars.full, bars.empty, slots, abort);
           if (*static_cast<volatile int*>(abort)) break;
         }
-        // after a time-out elsewhere, stay until the copies in flight have landed
-        if (*static_cast<volatile int*>(abort) && uses > 0)
-          mbar_wait_bounded(&bars.full[lane], (uses - 1) & 1, tmo, p.err, nullptr, true);
+        if (*static_cast<volatile int*>(abort)) feeder.drain(p, bars.full);
       } else if (warp == kWalk) {
         // ================================================================ walk
-        Cursor c = cursor_at<kRows>(p, kKeys, x0);
         ItemWriter out;
-        long long left = x1 - x0;
-        while (!*static_cast<volatile int*>(abort)) {
-          const int n = static_cast<int>(min(left, static_cast<long long>(c.u1 - c.u)));
-          out.put(bars.items, make_item<kRows>(p, c, n, blockIdx.x), tmo, p.err, abort);
-          if (left <= 0) break;  // that was the end mark
-          left -= n;
-          if (left > 0) cursor_next<kRows>(p, kKeys, c);
-        }
+        walk_range<kRows>(p, kKeys, blockIdx.x, x0, x1, range, [&](const Item& t) {
+          out.put(bars.items, t, tmo, p.err, abort);
+          return *static_cast<volatile int*>(abort) == 0;
+        });
       } else {
         // =================================================== matrix instructions
         // Warp kMma issues tile A's, kMma + 1 tile B's: what one waits for is
@@ -633,8 +581,7 @@ int launch(const AttnParams& p, cudaStream_t s) {
     }
     set[dev] = true;
   }
-  attn_tiles_kernel<D><<<p.blocks, kThreads, smem, s>>>(p, slots);
-  return check_launch();
+  return launch_after(attn_tiles_kernel<D>, dim3(p.blocks), kThreads, smem, s, p, slots);
 }
 
 }  // namespace
