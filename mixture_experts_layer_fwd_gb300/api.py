@@ -489,6 +489,12 @@ def _empty(shape, dtype, device, stream=None) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The cudaStream_t of `stream`, or of the current stream of t's device
+    (without building a torch.cuda.Stream, which costs as much as a launch)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+
+
 def _heads(t: torch.Tensor, name: str, T=None, D=None, device=None) -> None:
     """bf16 [T, heads, D] whose tokens may be apart (a slice of a projection's
     output): heads and D contiguous, any token stride."""
@@ -570,7 +576,7 @@ def moe_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: Optional[torch.T
     check(load().moe_qk_norm_rope(_ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), v_stride, T, Hq, Hkv,
                                   D, _ptr(wq), _ptr(wk), eps, _ptr(cos_sin), max_pos, rot, int(interleaved),
                                   _ptr(pos), _ptr(q_out), _ptr(k_out), _ptr(pool), num_pages, page_size, _ptr(g_k),
-                                  _ptr(g_v), _ptr(slots), _stream(stream)), "moe_qk_norm_rope")
+                                  _ptr(g_v), _ptr(slots), _raw_stream(stream, q)), "moe_qk_norm_rope")
     return q_out, k_out
 
 
@@ -610,7 +616,7 @@ def moe_kv4_attention(q: torch.Tensor, pool: torch.Tensor, g_k: torch.Tensor, g_
     check(lib.moe_kv4_attention(_ptr(q), _token_stride(q), T, Hq, _ptr(pool), pool.shape[0], page_size, Hkv, D,
                                 _ptr(g_k), _ptr(g_v), _ptr(q_offsets), _ptr(kv_lens), _ptr(table), B, max_pages,
                                 D ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), _ptr(lse),
-                                _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)), "moe_kv4_attention")
+                                _ptr(ws), ws.numel() * ws.element_size(), _raw_stream(stream, q)), "moe_kv4_attention")
     return out
 
 
@@ -675,7 +681,7 @@ def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: to
     ws = _empty(lib.moe_kv_pages_workspace_size(N, S), torch.uint8, dev, stream)
     check(lib.moe_kv_extend(_ptr(q_offsets), T, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
                             _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _ptr(r["slots"]), _ptr(r["pos"]),
-                            _ptr(ws), ws.numel(), _stream(stream)), "moe_kv_extend")
+                            _ptr(ws), ws.numel(), _raw_stream(stream, table)), "moe_kv_extend")
     return r
 
 
@@ -699,7 +705,7 @@ def moe_kv_fork(src: torch.Tensor, dst: torch.Tensor, table: torch.Tensor, lens:
     ws = _empty(lib.moe_kv_pages_workspace_size(N, max(S, n)), torch.uint8, dev, stream)
     check(lib.moe_kv_fork(_ptr(src), _ptr(dst), n, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
                           _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), base, layers, layer_stride, page_bytes,
-                          _ptr(ws), ws.numel(), _stream(stream)), "moe_kv_fork")
+                          _ptr(ws), ws.numel(), _raw_stream(stream, table)), "moe_kv_fork")
     return r
 
 
@@ -713,7 +719,7 @@ def moe_kv_free(rows: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, ref
              lens=_like(o.get("lens"), "lens", lens, inplace, stream),
              refs=_like(o.get("refs"), "refs", refs, inplace, stream))
     check(load().moe_kv_free(_ptr(rows), n, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
-                             _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _stream(stream)), "moe_kv_free")
+                             _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _raw_stream(stream, table)), "moe_kv_free")
     return r
 
 
@@ -730,7 +736,7 @@ def moe_kv_compact(table: torch.Tensor, refs: torch.Tensor, pool: Optional[torch
     lib = load()
     ws = _empty(lib.moe_kv_pages_workspace_size(N, 0), torch.uint8, dev, stream)
     check(lib.moe_kv_compact(_ptr(table), _ptr(refs), S, M, N, _ptr(r["table"]), _ptr(r["refs"]), _ptr(r["remap"]),
-                             base, layers, layer_stride, page_bytes, _ptr(ws), ws.numel(), _stream(stream)),
+                             base, layers, layer_stride, page_bytes, _ptr(ws), ws.numel(), _raw_stream(stream, table)),
           "moe_kv_compact")
     return r
 
@@ -744,7 +750,7 @@ def moe_kv_copy_pages(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, 
     if _index(dst, "dst", pool.device) != n:
         raise ValueError("dst: expected as many pages as src")
     check(load().moe_kv_copy_pages(base, layers, layer_stride, page_bytes, pool.shape[1], _ptr(src), _ptr(dst), n,
-                                   _stream(stream)), "moe_kv_copy_pages")
+                                   _raw_stream(stream, pool)), "moe_kv_copy_pages")
     return pool
 
 
