@@ -31,32 +31,69 @@ struct NormParams {
   const float *g_k, *g_v;
   const long long* slots;
   int chunks;  // warps per token
+  uint64_t neg_zero2;  // a pair of -0
   unsigned int* err;
 };
 
-// 8 values of one head per lane, D/8 lanes per head.
+// Packed fp32 pairs: each half one IEEE rounding.
+DEVINL uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+DEVINL void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+// a * b + (-0): the product rounded once, with its sign.  The zero comes from
+// the kernel's parameters because the assembler turns a constant one back into
+// a product and then contracts packed products with sums.
+DEVINL uint64_t mul2(uint64_t a, uint64_t b, uint64_t neg_zero) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(neg_zero));
+  return r;
+}
+DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A lane's 8 consecutive values (D/8 lanes per head) as pairs (0,2) (1,3) (4,6)
+// (5,7): the sum's neighbours and an interleaved rotation's partners face each
+// other in the two halves of two pairs.
+struct Eight {
+  uint64_t v[4];
+};
+DEVINL Eight from_bf16(const uint4& u) {
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
+  return Eight{{pack2(lo(u.x), lo(u.y)), pack2(hi(u.x), hi(u.y)), pack2(lo(u.z), lo(u.w)), pack2(hi(u.z), hi(u.w))}};
+}
+DEVINL Eight from_float(const float (&x)[8]) {
+  return Eight{{pack2(x[0], x[2]), pack2(x[1], x[3]), pack2(x[4], x[6]), pack2(x[5], x[7])}};
+}
+DEVINL void to_float(const Eight& e, float (&x)[8]) {
+  unpack2(e.v[0], x[0], x[2]);
+  unpack2(e.v[1], x[1], x[3]);
+  unpack2(e.v[2], x[4], x[6]);
+  unpack2(e.v[3], x[5], x[7]);
+}
+DEVINL uint4 to_bf16(const Eight& e) {
+  float x[8];
+  to_float(e, x);
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+
+// Sum of squares of a head, neighbours first.
 template <int D>
-DEVINL float head_sum(const float (&x)[8]) {
-  float s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(x[i], x[i]);
-#pragma unroll
-  for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-    for (int i = 0; i < w; ++i) s[i] = __fadd_rn(s[2 * i], s[2 * i + 1]);
-  float t = s[0];
+DEVINL float head_sum(const Eight& e, uint64_t nz) {
+  const uint64_t a = add2(mul2(e.v[0], e.v[0], nz), mul2(e.v[1], e.v[1], nz));  // (0+1, 2+3)
+  const uint64_t b = add2(mul2(e.v[2], e.v[2], nz), mul2(e.v[3], e.v[3], nz));
+  float a0, a1, b0, b1;
+  unpack2(a, a0, a1);
+  unpack2(b, b0, b1);
+  float t = __fadd_rn(__fadd_rn(a0, a1), __fadd_rn(b0, b1));
 #pragma unroll
   for (int o = 1; o < D / 8; o <<= 1) t = __fadd_rn(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
   return t;
-}
-
-DEVINL void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
 }
 
 // The lane's 8 values (half a block of 16; lanes 2j and 2j+1 share it) as
@@ -75,12 +112,92 @@ DEVINL uint32_t quantise8(const float (&v)[8], float g, uint32_t& s) {
   return e2m1x8_rn_satfinite(q);
 }
 
+// What a lane needs of its token and place.
+template <int D, bool PAIRS>
+struct Lane {
+  int l, sub;     // lane in the head, head in the warp's step
+  bool turns;     // its values are rotated
+  int partner;    // lane with the other half of its pairs
+  Eight c, s;     // signed: y = x * c + partner * s for either half
+  uint8_t* page;  // the token's page in the cache, or null
+  int off;
+};
+
+// Norm, rotation and output of `n` <= U groups of heads from h0 on.  The
+// inverse roots of U groups are formed side by side, one in each of four
+// neighbouring lanes: an IEEE root and reciprocal cost as much as the rest.
+template <int D, bool PAIRS, int U>
+DEVINL void heads_step(const NormParams& p, const Lane<D, PAIRS>& L, const uint16_t* src, int h0, int n, int heads,
+                       bool norm, const Eight& w, uint16_t* dst, bool cache) {
+  constexpr int HPW = 256 / D;
+  const int lane = threadIdx.x & 31;
+  const uint64_t nz = p.neg_zero2;
+  uint4 raw[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int h = h0 + u * HPW + L.sub;
+    raw[u] = make_uint4(0, 0, 0, 0);
+    if (u < n && h < heads) raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * D + 8 * L.l));
+  }
+  float r[U];
+  if (norm) {
+    float mine = 0.0f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float t = head_sum<D>(from_bf16(raw[u]), nz);
+      if (U == 1 || (lane & (U - 1)) == u) mine = t;
+    }
+    mine = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(mine, 1.0f / D), p.eps)));
+#pragma unroll
+    for (int u = 0; u < U; ++u) r[u] = U == 1 ? mine : __shfl_sync(0xFFFFFFFFu, mine, (lane & ~(U - 1)) | u);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (u >= n) break;
+    const int h = h0 + u * HPW + L.sub;
+    Eight x = from_bf16(raw[u]);
+    if (norm) {
+      const uint64_t rr = pack2(r[u], r[u]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.v[i] = mul2(mul2(x.v[i], rr, nz), w.v[i], nz);
+    }
+    if (p.rot > 0) {
+      Eight y;
+      if (PAIRS) {
+        y = Eight{{x.v[1], x.v[0], x.v[3], x.v[2]}};
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y.v[i] = __shfl_sync(0xFFFFFFFFu, x.v[i], L.partner);
+      }
+      if (L.turns) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.v[i] = add2(mul2(x.v[i], L.c.v[i], nz), mul2(y.v[i], L.s.v[i], nz));
+      }
+    }
+    const bool have = h < heads;
+    if (dst != nullptr && have) *reinterpret_cast<uint4*>(dst + h * D + 8 * L.l) = to_bf16(x);
+    if (cache) {
+      float f[8];
+      to_float(x, f);
+      uint32_t sf;
+      const uint32_t codes = quantise8(f, __ldg(p.g_k + min(h, heads - 1)), sf);
+      if (have && L.page != nullptr) {
+        uint8_t* sec = L.page + static_cast<long long>(h) * kv4::record_bytes(p.P, D);
+        *reinterpret_cast<uint32_t*>(sec + L.off * (D / 2) + 4 * L.l) = codes;
+        if ((L.l & 1) == 0) sec[kv4::codes_bytes(p.P, D) + L.off * (D / 16) + L.l / 2] = static_cast<uint8_t>(sf);
+      }
+    }
+  }
+}
+
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormParams p) {
   constexpr int LPH = D / 8;     // lanes per head
   constexpr int HPW = 32 / LPH;  // heads per warp step
   const int lane = threadIdx.x & 31;
-  const int l = lane % LPH, sub = lane / LPH;
+  Lane<D, PAIRS> L;
+  L.l = lane % LPH, L.sub = lane / LPH;
+  const int l = L.l;
   const long long wid = (static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
   const int t = static_cast<int>(wid / p.chunks), chunk = static_cast<int>(wid % p.chunks);
   if (t >= p.T) return;
@@ -90,7 +207,6 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormParams
   const int g0 = static_cast<int>(static_cast<long long>(groups) * chunk / p.chunks);
   const int g1 = static_cast<int>(static_cast<long long>(groups) * (chunk + 1) / p.chunks);
 
-  // this lane's rotation: signed so that y = x * c + partner * s for either half
   float c[8], s[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -98,8 +214,8 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormParams
     s[i] = 0.0f;
   }
   const int half = p.rot / 2, hl = half / 8;  // pairs, and lanes that hold the first half
-  const bool turns = 8 * l < p.rot;
-  if (turns) {
+  L.turns = 8 * l < p.rot;
+  if (L.turns) {
     int at = __ldg(p.pos + t);
     if (at < 0 || at >= p.max_pos) {
       if (l == 0 && chunk == 0) atomicOr(p.err, kErrBadIndex);
@@ -128,76 +244,57 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const NormParams
       }
     }
   }
-  const int partner = sub * LPH + (!turns ? l : l < hl ? l + hl : l - hl);
-
-  uint8_t* page = nullptr;
-  int off = 0;
+  L.c = from_float(c), L.s = from_float(s);
+  L.partner = L.sub * LPH + (!L.turns ? l : l < hl ? l + hl : l - hl);
+  L.page = nullptr, L.off = 0;
   if (p.pool != nullptr && g1 > nq) {
     const long long slot = __ldg(p.slots + t);
     if (slot >= static_cast<long long>(p.num_pages) * p.P) {
       if (lane == 0) atomicOr(p.err, kErrBadIndex);
     } else if (slot >= 0) {
-      page = p.pool + (slot / p.P) * p.Hkv * kv4::record_bytes(p.P, D);
-      off = static_cast<int>(slot % p.P);
+      L.page = p.pool + (slot / p.P) * p.Hkv * kv4::record_bytes(p.P, D);
+      L.off = static_cast<int>(slot % p.P);
     }
   }
 
-  for (int g = g0; g < g1; g += kUnroll) {
-    uint4 raw[kUnroll];
+  const Eight one = Eight{{0, 0, 0, 0}};
+  if (g0 < nq) {
+    const Eight w = p.wq ? from_bf16(__ldg(reinterpret_cast<const uint4*>(p.wq + 8 * l))) : one;
+    const uint16_t* src = p.q + t * p.q_stride;
+    uint16_t* dst = p.q_out + static_cast<long long>(t) * p.Hq * D;
+    for (int g = g0; g < min(g1, nq); g += kUnroll)
+      heads_step<D, PAIRS, kUnroll>(p, L, src, g * HPW, min(g1, nq) - g, p.Hq, p.wq != nullptr, w, dst, false);
+  }
+  if (g1 > nq && g0 < nq + nk) {
+    const Eight w = p.wk ? from_bf16(__ldg(reinterpret_cast<const uint4*>(p.wk + 8 * l))) : one;
+    const uint16_t* src = p.k + t * p.k_stride;
+    uint16_t* dst = p.k_out ? p.k_out + static_cast<long long>(t) * p.Hkv * D : nullptr;
+    const int first = max(g0, nq) - nq, last = min(g1 - nq, nk);
+    for (int g = first; g < last; g += 2)
+      heads_step<D, PAIRS, 2>(p, L, src, g * HPW, last - g, p.Hkv, p.wk != nullptr, w, dst, p.pool != nullptr);
+  }
+  // values: two groups of heads at a time
+  for (int g = max(g0 - nq - nk, 0); g < g1 - nq - nk; g += 2) {
+    const uint16_t* src = p.v + t * p.v_stride;
+    uint4 raw[2];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < 2; ++u) {
+      const int h = (g + u) * HPW + L.sub;
       raw[u] = make_uint4(0, 0, 0, 0);
-      const int gu = g + u;
-      if (gu >= g1) continue;
-      const int kind = gu < nq ? 0 : gu < nq + nk ? 1 : 2;
-      const int h = (gu - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * HPW + sub;
-      const uint16_t* src = kind == 0 ? p.q + t * p.q_stride : kind == 1 ? p.k + t * p.k_stride : p.v + t * p.v_stride;
-      if (h < (kind == 0 ? p.Hq : p.Hkv)) raw[u] = *reinterpret_cast<const uint4*>(src + h * D + 8 * l);
+      if (g + u < g1 - nq - nk && h < p.Hkv) raw[u] = __ldcs(reinterpret_cast<const uint4*>(src + h * D + 8 * l));
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int gu = g + u;
-      if (gu >= g1) break;
-      const int kind = gu < nq ? 0 : gu < nq + nk ? 1 : 2;
-      const int h = (gu - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * HPW + sub;
-      const bool have = h < (kind == 0 ? p.Hq : p.Hkv);
+    for (int u = 0; u < 2; ++u) {
+      if (g + u >= g1 - nq - nk) break;
+      const int h = (g + u) * HPW + L.sub;
       float x[8];
-      unpack8(raw[u], x);
-      if (kind < 2) {
-        const uint16_t* w = kind == 0 ? p.wq : p.wk;
-        if (w != nullptr) {
-          const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(head_sum<D>(x), 1.0f / D), p.eps)));
-          float wf[8];
-          unpack8(__ldg(reinterpret_cast<const uint4*>(w + 8 * l)), wf);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), wf[i]);
-        }
-        if (p.rot > 0) {
-          float y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = PAIRS ? x[i ^ 1] : __shfl_sync(0xFFFFFFFFu, x[i], partner);
-          if (turns) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i], s[i]));
-          }
-        }
-        uint16_t* dst = kind == 0 ? p.q_out : p.k_out;
-        if (dst != nullptr && have) {
-          dst += (static_cast<long long>(t) * (kind == 0 ? p.Hq : p.Hkv) + h) * D + 8 * l;
-          *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                                                      pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-        }
-      }
-      if (kind > 0 && p.pool != nullptr) {
-        uint32_t sf;
-        const float gs = __ldg((kind == 1 ? p.g_k : p.g_v) + min(h, p.Hkv - 1));
-        const uint32_t codes = quantise8(x, gs, sf);
-        if (have && page != nullptr) {
-          uint8_t* sec = page + static_cast<long long>(h) * kv4::record_bytes(p.P, D) +
-                         (kind == 2 ? kv4::record_bytes(p.P, D) / 2 : 0);
-          *reinterpret_cast<uint32_t*>(sec + off * (D / 2) + 4 * l) = codes;
-          if ((l & 1) == 0) sec[kv4::codes_bytes(p.P, D) + off * (D / 16) + l / 2] = static_cast<uint8_t>(sf);
-        }
+      to_float(from_bf16(raw[u]), x);
+      uint32_t sf;
+      const uint32_t codes = quantise8(x, __ldg(p.g_v + min(h, p.Hkv - 1)), sf);
+      if (h < p.Hkv && L.page != nullptr) {
+        uint8_t* sec = L.page + static_cast<long long>(h) * kv4::record_bytes(p.P, D) + kv4::record_bytes(p.P, D) / 2;
+        *reinterpret_cast<uint32_t*>(sec + L.off * (D / 2) + 4 * l) = codes;
+        if ((l & 1) == 0) sec[kv4::codes_bytes(p.P, D) + L.off * (D / 16) + l / 2] = static_cast<uint8_t>(sf);
       }
     }
   }
@@ -230,7 +327,7 @@ extern "C" int moe_qk_norm_rope(const uint16_t* q, long long q_stride, const uin
       k_stride < static_cast<long long>(Hkv) * D || (pool && (v_stride % 8 || v_stride < static_cast<long long>(Hkv) * D)))
     return MOE_ERR_INVALID_ARG;
   NormParams p{q, k, v, q_stride, k_stride, v_stride, T, Hq, Hkv, wq, wk, eps, cos_sin, max_pos, rot, pos, q_out, k_out,
-               pool, num_pages, page_size, g_k, g_v, slots, 1, device_error_word()};
+               pool, num_pages, page_size, g_k, g_v, slots, 1, 0x8000000080000000ull, device_error_word()};
   if (!p.err) return MOE_ERR_CUDA;
   const int hpw = 256 / D;
   const int groups = (Hq + hpw - 1) / hpw + (pool ? 2 : 1) * ((Hkv + hpw - 1) / hpw);
