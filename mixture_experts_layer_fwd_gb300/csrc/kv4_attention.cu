@@ -26,9 +26,9 @@ namespace {
 
 constexpr int kRows = kRowsSmall;
 constexpr int kWarps = 4;     // consumer warps of a group
-constexpr int kGroups = 3;    // groups of a block, each with its own range of the work
+constexpr int kGroups = 3;    // groups of a block at most, each with its own range of the work
 constexpr int kThreads = 32 * kGroups * kWarps + 128;  // and a warpgroup with their producers
-constexpr int kMaxStages = 16;
+constexpr int kMaxSlots = 32;
 constexpr int kSmem = 226 * 1024;
 
 // ------------------------------------------------------------------ schedule
@@ -218,7 +218,7 @@ DEVINL void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
 // One group's shared memory beside its ring: 4 consumer warps share it.
 template <int D>
 struct Group {
-  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t full[kMaxSlots], empty[kMaxSlots];  // warp w's ring: slots w * slots of a warp ..
   ItemRing items;
   float m[kWarps][kRows], l[kWarps][kRows];
   int abort;
@@ -226,22 +226,22 @@ struct Group {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnParams p, int stages) {
+__global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnParams p, int groups, int slots) {
   constexpr int KS = D / 16;  // k steps of S
   constexpr int LD = D / 4;   // values of a key per lane (S), of a row of O per lane
   constexpr int NT = D / 8;   // column tiles of O
   constexpr int W = D / 64;   // words of a value row per lane
   extern __shared__ __align__(128) uint8_t smem[];
-  const int rec = record_bytes(p.P, D);
+  const int rec = record_bytes(p.P, D), hb = rec / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp < kGroups * kWarps ? warp / kWarps : warp - kGroups * kWarps;
   constexpr int head = (sizeof(Group<D>) + 127) & ~127;
-  uint8_t* mine = smem + min(grp, kGroups - 1) * (head + stages * rec);
+  uint8_t* mine = smem + min(grp, groups - 1) * (head + kWarps * slots * hb);
   Group<D>& sh = *reinterpret_cast<Group<D>*>(mine);
   uint8_t* ring = mine + head;
 
-  if (warp < kGroups * kWarps && warp % kWarps == 0 && lane == 0) {
-    for (int i = 0; i < stages; ++i) {
+  if (warp < groups * kWarps && warp % kWarps == 0 && lane == 0) {
+    for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
@@ -253,35 +253,49 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
 
   launch_dependents();
   wait_for_previous();
-  const int block = blockIdx.x * kGroups + grp;  // the group's range
+  const int block = blockIdx.x * groups + grp;  // the group's range
   const long long total = total_units(p), range = range_of(p, total);
   const long long x0 = block * range, x1 = min(total, x0 + range);
   int* const abort = &sh.abort;
 
   if (warp >= kGroups * kWarps) {
-    // -------- one warp per group walks its range and feeds its ring, a page record per stage
+    // -------- one warp per group walks its range and feeds the four warps' rings
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (grp >= kGroups) return;
+    if (grp >= groups) return;
     ItemWriter out;
-    Feeder feeder;
+    const int w = lane / slots;  // whose ring; its units of an item are every fourth
+    Slot slot;
+    slot.index = lane % slots, slot.slots = slots;
+    slot.to = w < kWarps ? ring + lane * hb : nullptr;
+    slot.full = &sh.full[lane], slot.empty = &sh.empty[lane];
+    uint32_t it = 0;  // units of the group so far
     walk_range<kRows>(p, p.P, block, x0, x1, range, [&](const Item& t) {
       out.put(sh.items, t, p.timeout_ns, p.err, abort);
-      if (t.n > 0)
-        feeder.feed(
-            p, t, t.n, rec, rec, [&](int k) { return t.u + k; }, [](int) { return 0; }, ring, sh.full, sh.empty, stages,
-            abort);
+      if (t.n > 0) {
+        const int first = (w - static_cast<int>(it)) & (kWarps - 1);
+        const int mine = first < t.n ? (t.n - first + kWarps - 1) / kWarps : 0;
+        slot.feed(
+            p, t, 2 * mine, hb, rec, [&](int k) { return t.u + first + kWarps * (k >> 1); },
+            [&](int k) { return k & 1 ? hb : 0; }, abort);
+        it += t.n;
+      }
       return *static_cast<volatile int*>(abort) == 0;
     });
-    if (*static_cast<volatile int*>(abort)) feeder.drain(p, sh.full);
+    if (*static_cast<volatile int*>(abort)) slot.drain(p);
     return;
   }
 
-  // -------- consumers: warp w of the group takes the stages w, w + 4, ...
+  // -------- consumers: warp w of the group takes the units w, w + 4, ...
+  if (grp >= groups) return;
   asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
   const int wg = warp % kWarps;
   const int g = lane >> 2, c4 = lane & 3;
   ItemReader items;
-  uint32_t it = 0;
+  uint32_t it = 0;   // units of the group so far
+  int st = 0;        // slot of the warp's next half record, and its parity
+  uint32_t par = 0;
+  const uint8_t* my_ring = ring + wg * slots * hb;
+  uint64_t *full = sh.full + wg * slots, *empty = sh.empty + wg * slots;
   while (true) {
     const Item t = items.next(sh.items, p.timeout_ns, p.err, abort);
     if (named_bar_red_or(1 + grp, 32 * kWarps, t.n == 0)) return;  // all four together
@@ -334,15 +348,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
     }
 
     for (int i = (wg - static_cast<int>(it)) & (kWarps - 1); i < n; i += kWarps) {
-      const uint32_t at = it + i;
-      const int st = at % stages;
-      wait_warp(&sh.full[st], (at / stages) & 1, p.timeout_ns, p.err, abort);
-      const uint8_t* kc = ring + static_cast<size_t>(st) * rec;
+      // keys in slot st, values in the next one
+      const int sv = st + 1 == slots ? 0 : st + 1;
+      const uint32_t pv = par ^ static_cast<uint32_t>(sv == 0);
+      const uint8_t* kc = my_ring + st * hb;
       const uint8_t* ks = kc + codes_bytes(p.P, D);
-      const uint8_t* vc = kc + rec / 2;
+      const uint8_t* vc = my_ring + sv * hb;
       const uint8_t* vs = vc + codes_bytes(p.P, D);
       const int key0 = (t.u + i) * p.P;
       const int keys = min(p.P, t.len - key0);
+      wait_warp(&full[st], par, p.timeout_ns, p.err, abort);
+      if (keys <= 0) {  // a unit without keys
+        if (lane == 0) mbar_arrive(&empty[st]);
+        wait_warp(&full[sv], pv, p.timeout_ns, p.err, abort);
+      }
 #pragma unroll 1
       for (int t0 = 0; t0 < keys; t0 += 32) {
         float s[4][4];
@@ -375,8 +394,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
             mma_f16(s[kt], qa[2 * j + 1], h[2], h[3]);
           }
         }
+        if (t0 + 32 >= keys) {  // the last of the unit's keys
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&empty[st]);
+        }
         const int k0 = key0 + t0;
-        if (k0 < all_lo || k0 + 32 > all_hi) {  // some row does not see all of these keys
+        if (__any_sync(0xFFFFFFFFu, k0 < all_lo || k0 + 32 > all_hi)) {  // some row does not see all of these keys
 #pragma unroll
           for (int kt = 0; kt < 4; ++kt)
 #pragma unroll
@@ -428,18 +451,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
             pa[kt >> 1][2 * (kt & 1) + half] = pack_f16x2(a, b);
           }
         }
-        const bool tail = t0 + 32 > keys;  // some of these keys were never written
+        if (t0 == 0) {
+          wait_warp(&full[sv], pv, p.timeout_ns, p.err, abort);
+          if (__any_sync(0xFFFFFFFFu, keys < p.P)) {
+            // values of keys that were never written: zero scales in the slot,
+            // which is the warp's until it hands it back
+            uint8_t* z = const_cast<uint8_t*>(vs);
+            for (int b = keys * (D / 16) + lane; b < p.P * (D / 16); b += 32) z[b] = 0;
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           uint32_t wa[2][W], wb[2][W], f[2];
 #pragma unroll
           for (int pr = 0; pr < 2; ++pr) {
             const int ta = t0 + 16 * kb + 8 * pr + ((2 * c4) ^ (c4 & 1)), tb = ta ^ 1;
-            uint32_t sa = vs[ta * (D / 16) + (D == 128 ? g : g >> 1)], sb = vs[tb * (D / 16) + (D == 128 ? g : g >> 1)];
-            if (tail) {
-              if (ta >= keys) sa = 0;
-              if (tb >= keys) sb = 0;
-            }
+            const uint32_t sa = vs[ta * (D / 16) + (D == 128 ? g : g >> 1)];
+            const uint32_t sb = vs[tb * (D / 16) + (D == 128 ? g : g >> 1)];
             f[pr] = e4m3x2_to_f16x2(sa | (sb << 8));
             if (W == 2) {
               const uint2 va = *reinterpret_cast<const uint2*>(vc + ta * (D / 2) + 8 * g);
@@ -469,7 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.empty[st]);
+      if (lane == 0) mbar_arrive(&empty[sv]);
+      st = sv, par = pv;
+      if (++st == slots) st = 0, par ^= 1;
     }
     it += n;
 
@@ -547,12 +579,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
   }
 }
 
+// Groups per block: three, but two where a warp's two half records are 18 KB.
+int groups_of(int P, int D) { return P * D > 64 * 128 ? 2 : kGroups; }
+
 template <int D>
 int launch_rows16(const AttnParams& p, cudaStream_t s) {
-  const int rec = record_bytes(p.P, D);
+  const int half = record_bytes(p.P, D) / 2;
   const int head = static_cast<int>(round_up(sizeof(Group<D>), 128));
-  const int stages = std::min(kMaxStages, (kSmem / kGroups - head) / rec);
-  const int smem = kGroups * (head + stages * rec);
+  const int groups = groups_of(p.P, D);
+  // half records per warp: two at least (a unit's keys and values)
+  const int slots = std::min(kMaxSlots / kWarps, (kSmem / groups - head) / (kWarps * half));
+  const int smem = groups * (head + kWarps * slots * half);
   static bool set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
@@ -564,7 +601,7 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
     }
     set[dev] = true;
   }
-  return launch_after(attn_rows16_kernel<D>, dim3(p.blocks / kGroups), kThreads, smem, s, p, stages);
+  return launch_after(attn_rows16_kernel<D>, dim3(p.blocks / groups), kThreads, smem, s, p, groups, slots);
 }
 
 // Schedule, main kernel, joining.
@@ -591,7 +628,7 @@ Layout layout(AttnParams& p, int D, void* ws) {
   // Up to 32 rows per sequence and kv head on average: 16 rows at a time.
   const bool tiles16 = static_cast<long long>(p.T) * p.G <= 32ll * p.B;
   r.rows = tiles16 ? kRows : kTileRows;
-  r.blocks = tiles16 ? kGroups * num_sms() : num_sms();
+  r.blocks = tiles16 ? groups_of(p.P, D) * num_sms() : num_sms();
   Carve c(ws, 0);
   const long long tiles = static_cast<long long>(p.T) * p.G / r.rows + p.B + 1;
   p.starts = c.take<int>(p.B + 1);
@@ -621,7 +658,7 @@ using namespace moe;
 extern "C" size_t moe_kv4_attention_workspace_size(int T, int B, int Hq, int Hkv, int D) {
   if (T < 1 || B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || !kv4::head_dim_ok(D)) return 0;
   kv4::AttnParams p{};
-  p.T = T, p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
+  p.T = T, p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.P = 64;  // the most blocks
   return kv4::layout(p, D, nullptr).bytes;
 }
 

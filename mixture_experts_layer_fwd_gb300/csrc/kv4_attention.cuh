@@ -312,24 +312,29 @@ struct PartItem {
 };
 static_assert(sizeof(PartItem) == 32, "eight words");
 
-// One lane's side of a ring of stages that bulk copies fill: lane l feeds slot
-// l, each at its own pace (one thread feeding all slots took about 900 cycles
-// per copy, in waits and barrier round trips).  An item's copies k = 0 .. all-1
-// take page_of(k) of its table row (one past the item's keys: nothing is
-// copied) from byte offset_of(k) of the record on.
-struct Feeder {
-  uint32_t uses = 0;  // of the lane's slot
-  int at = 0;         // slot of the item's first copy
+// One lane's slot of a ring that bulk copies fill.  Each lane feeds its slot at
+// its own pace (one thread feeding all slots took about 900 cycles per copy, in
+// waits and barrier round trips).  A ring has ONE consumer, a warp or a team
+// that waits together: it takes the uses of a slot in order, so that a barrier's
+// parity names the use it waits for.  (A consumer that could be ahead of another
+// one's use of the same slot would pass on the phase before.)
+struct Slot {
+  uint8_t* to;             // null: the lane feeds none
+  uint64_t *full, *empty;  // count 1; count: arrivals of the consumer
+  int index, slots;        // in its ring
+  uint32_t uses = 0;
+  int at = 0;              // slot of the item's first copy
+  // Copies k = 0 .. all-1 of the ring, `bytes` each: from byte offset_of(k) of
+  // the record of page page_of(k) of the item's table row (past the item's
+  // keys: nothing is copied).  A whole warp calls it.
   template <class PageOf, class OffsetOf>
   DEVINL void feed(const AttnParams& p, const Item& it, int all, int bytes, int rec, PageOf page_of,
-                   OffsetOf offset_of, uint8_t* ring, uint64_t* full, uint64_t* empty, int slots,
-                   volatile int* abort) {
-    const int lane = threadIdx.x & 31;
+                   OffsetOf offset_of, volatile int* abort) {
     const uint8_t* pool = p.pool + static_cast<long long>(it.h) * rec;
     const long long stride = static_cast<long long>(p.Hkv) * rec;
     const int32_t* table = p.table + static_cast<long long>(it.b) * p.max_pages;
     const int last = (it.len + p.P - 1) / p.P;
-    int k = lane < slots ? (lane >= at ? lane - at : lane - at + slots) : all;
+    int k = to != nullptr ? (index >= at ? index - at : index - at + slots) : all;
     int id = -2;  // page of copy k: -2 not looked up, -1 none
     uint64_t t0 = 0;
     while (__any_sync(0xFFFFFFFFu, k < all)) {
@@ -346,12 +351,12 @@ struct Feeder {
             }
           }
         }
-        if (uses == 0 || mbar_test_wait(&empty[lane], (uses - 1) & 1)) {
+        if (uses == 0 || mbar_test_wait(empty, (uses - 1) & 1)) {
           if (id < 0) {
-            mbar_arrive(&full[lane]);  // no key of this page
+            mbar_arrive(full);  // no key of this page
           } else {
-            mbar_arrive_expect_tx(&full[lane], bytes);
-            bulk_load(ring + lane * bytes, pool + id * stride + offset_of(k), bytes, &full[lane]);
+            mbar_arrive_expect_tx(full, bytes);
+            bulk_load(to, pool + id * stride + offset_of(k), bytes, full);
           }
           ++uses;
           k += slots;
@@ -372,11 +377,11 @@ struct Feeder {
         __nanosleep(100);
       }
     }
-    at = (at + all) % slots;
+    if (to != nullptr) at = (at + all) % slots;
   }
   // After a time-out elsewhere: stay until the copies in flight have landed.
-  DEVINL void drain(const AttnParams& p, uint64_t* full) {
-    if (uses > 0) mbar_wait_bounded(&full[threadIdx.x & 31], (uses - 1) & 1, p.timeout_ns, p.err, nullptr, true);
+  DEVINL void drain(const AttnParams& p) {
+    if (uses > 0) mbar_wait_bounded(full, (uses - 1) & 1, p.timeout_ns, p.err, nullptr, true);
   }
 };
 

@@ -44,12 +44,12 @@ struct Cfg {
   static constexpr int SUB_Q = 128 * 128;         // 64-wide sub-tile of Q or K
   static constexpr int SUB_V = D * 128;           // 64-key sub-tile of V transposed
   static constexpr int BARS0 = 2 * Q_BYTES + 4 * K_BYTES;
-  static constexpr int RING0 = BARS0 + 3072;
+  static constexpr int RING0 = BARS0 + 3328;
   static constexpr int RING = (D == 128 ? 227 : 160) * 1024 - RING0;
 };
 
 struct Bars {
-  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];  // rings of key and of value halves
   uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
   uint64_t qfull[2], sfull[2], pfull[2], ofull[2], turn[2], done;
   ItemRing items;
@@ -57,7 +57,7 @@ struct Bars {
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 3072, "between the operand tiles and the ring");
+static_assert(sizeof(Bars) <= 3328, "between the operand tiles and the ring");
 
 // D[tmem] (+)= A[smem] * B[smem]^T from a whole converged warp.
 DEVINL void umma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -108,7 +108,7 @@ DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, int h, u
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParams p, int slots) {
+__global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParams p, int k_slots, int v_slots) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   // 1024-byte aligned operand tiles: Q_A Q_B | K0 K1 | V0 V1 | barriers | ring of record halves
@@ -119,11 +119,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = record_bytes(p.P, D) / 2, pages = kKeys / p.P;
   const unsigned long long tmo = p.timeout_ns;
+  const int slots[2] = {k_slots, v_slots};
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < slots; ++i) {
-      mbar_init(&bars.full[i], 1);
-      mbar_init(&bars.empty[i], 4);
+    for (int i = 0; i < 2 * kMaxSlots; ++i) {
+      mbar_init(&bars.full[0][i], 1);
+      mbar_init(&bars.empty[0][i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.kfull[i], 4);
@@ -343,12 +344,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         const int blk = D == 128 ? (2 * (tg >> 1) + (lane >> 3) + 4 * (w >> 1)) & 7 : (2 * (tg >> 1) + (lane >> 3)) & 3;
         const int odd = tg & 1;
         const int logp = p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
-        int slot = is_v ? pages : 0;  // of the ring's next half for these warps: K and V halves take turns
-        uint32_t round = 0;           // its parity
+        const int n_slots = is_v ? v_slots : k_slots;
+        const uint8_t* my_ring = ring + (is_v ? k_slots * half : 0);
+        uint64_t *full = bars.full[is_v], *empty = bars.empty[is_v];
+        int slot = 0;        // of the team's next half
+        uint32_t round = 0;  // its parity
         // Byte offset of a key's half, the key counted in the tile.
         auto half_of = [&](int key) {
           int sl = slot + (key >> logp);
-          if (sl >= slots) sl -= slots;
+          if (sl >= n_slots) sl -= n_slots;
           return sl * half;
         };
         ItemReader items;
@@ -362,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               int sl = slot;
               uint32_t rd = round;
               for (int pg = 0; pg < pages; ++pg) {
-                wait_warp(&bars.full[sl], rd, tmo, p.err, abort);
-                if (++sl == slots) sl = 0, rd ^= 1;
+                wait_warp(&full[sl], rd, tmo, p.err, abort);
+                if (++sl == n_slots) sl = 0, rd ^= 1;
               }
             }
             if (w == 0 && j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, tmo, p.err, abort);
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const int in = (32 * (k2 + k) + key0) & (p.P - 1);
-                const uint8_t* kc = ring + half_of(32 * (k2 + k));
+                const uint8_t* kc = my_ring + half_of(32 * (k2 + k));
                 if (W == 4) {
                   const uint4 v = *reinterpret_cast<const uint4*>(kc + in * (D / 2) + 16 * c4);
                   cw[k][0] = v.x, cw[k][1] = v.y, cw[k][2 % W] = v.z, cw[k][3 % W] = v.w;
@@ -411,8 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               // thread = (8 keys, block of 16 values)
               const int first = tgh * 64 + tg * 8;
               const int in = first & (p.P - 1);
-              const uint8_t* vc = ring + half_of(first) + in * (D / 2) + 8 * blk;
-              const uint8_t* vs = ring + half_of(first) + codes_bytes(p.P, D) + in * (D / 16) + blk;
+              const uint8_t* vc = my_ring + half_of(first) + in * (D / 2) + 8 * blk;
+              const uint8_t* vs = my_ring + half_of(first) + codes_bytes(p.P, D) + in * (D / 16) + blk;
               // register q holds key q ^ odd, so that neighbours read different banks
               const uint8_t *vc0 = vc + odd * (D / 2), *vc1 = vc - odd * (D / 2);
               uint2 cw[8];
@@ -455,9 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(is_v ? &bars.vfull[st] : &bars.kfull[st]);
-            for (int pg = 0; pg < 2 * pages; ++pg) {
-              if (pg < pages && lane == 0) mbar_arrive(&bars.empty[slot]);
-              if (++slot == slots) slot = 0, round ^= 1;
+            for (int pg = 0; pg < pages; ++pg) {
+              if (lane == 0) mbar_arrive(&empty[slot]);
+              if (++slot == n_slots) slot = 0, round ^= 1;
             }
           }
         }
@@ -465,19 +469,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
        if (warp == kLoad) {
         // ================================================================ load
-        Feeder feeder;
+        // lanes 0 .. feed the keys' ring, 16 .. the values'
+        const int v = lane >> 4, i = lane & 15;
+        Slot slot;
+        slot.index = i, slot.slots = slots[v];
+        slot.to = i < slots[v] ? ring + ((v ? slots[0] : 0) + i) * half : nullptr;
+        slot.full = &bars.full[v][i], slot.empty = &bars.empty[v][i];
         ItemReader items;
-        const int shift = pages == 1 ? 1 : pages == 2 ? 2 : 3;  // halves of a tile: keys of its pages, then values
         while (true) {
           const Item it = items.next(bars.items, tmo, p.err, abort);
           if (it.n == 0) break;
-          feeder.feed(
-              p, it, 2 * pages * it.n, half, 2 * half,
-              [&](int k) { return it.u * pages + (k >> shift) * pages + (k & (pages - 1)); },
-              [&](int k) { return (k & pages) ? half : 0; }, ring, bars.full, bars.empty, slots, abort);
+          slot.feed(
+              p, it, pages * it.n, half, 2 * half, [&](int k) { return it.u * pages + k; },
+              [&](int) { return v ? half : 0; }, abort);
           if (*static_cast<volatile int*>(abort)) break;
         }
-        if (*static_cast<volatile int*>(abort)) feeder.drain(p, bars.full);
+        if (*static_cast<volatile int*>(abort)) slot.drain(p);
       } else if (warp == kWalk) {
         // ================================================================ walk
         ItemWriter out;
@@ -567,8 +574,10 @@ template <int D>
 int launch(const AttnParams& p, cudaStream_t s) {
   using C = Cfg<D>;
   const int half = record_bytes(p.P, D) / 2;
-  const int slots = std::min(kMaxSlots, C::RING / half);
-  const int smem = C::RING0 + slots * half;
+  // a tile's halves at least, the rest shared out, keys first
+  const int all = std::min(2 * kMaxSlots, C::RING / half);
+  const int k_slots = (all + 1) / 2, v_slots = all / 2;
+  const int smem = C::RING0 + all * half;
   static bool set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
@@ -581,7 +590,7 @@ int launch(const AttnParams& p, cudaStream_t s) {
     }
     set[dev] = true;
   }
-  return launch_after(attn_tiles_kernel<D>, dim3(p.blocks), kThreads, smem, s, p, slots);
+  return launch_after(attn_tiles_kernel<D>, dim3(p.blocks), kThreads, smem, s, p, k_slots, v_slots);
 }
 
 }  // namespace
