@@ -1,0 +1,72 @@
+"""A paged NVFP4 key/value cache for a batch of sequences: owns the pools of all
+layers, the block table, the lengths and the pages' counts, and runs the
+library's cache calls on them.
+
+Everything stays on the device: a step's new tokens are placed by
+moe_kv_extend, written by moe_qk_norm_rope and read by moe_kv4_attention, all
+on the current stream, without a host read.
+"""
+from __future__ import annotations
+
+from typing import List, Optional, Sequence
+
+import torch
+
+from . import api
+
+
+class KV4Cache:
+    def __init__(self, layers: int, num_pages: int, rows: int, max_pages: int, Hkv: int, D: int, g_k: torch.Tensor,
+                 g_v: torch.Tensor, page_size: int = 64):
+        """rows: sequences at a time; max_pages: pages of the longest one; g_k,
+        g_v fp32 [layers, Hkv]: the global scale of each kv head's keys and
+        values (their largest magnitude / 2688, from calibration)."""
+        if page_size not in (32, 64, 128) or D not in (64, 128):
+            raise ValueError("page_size: expected 32, 64 or 128; D: expected 64 or 128")
+        for name, g in (("g_k", g_k), ("g_v", g_v)):
+            api._dev(g, name, dtype=torch.float32, shape=(layers, Hkv))
+        dev = g_k.device
+        self.layers, self.page_size, self.Hkv, self.D, self.device = layers, page_size, Hkv, D, dev
+        self.g_k, self.g_v = g_k, g_v
+        self.pool = torch.empty(layers, num_pages, Hkv, page_size * D * 9 // 8, dtype=torch.uint8, device=dev)
+        self.table = torch.full((rows, max_pages), -1, dtype=torch.int32, device=dev)
+        self.lens = torch.zeros(rows, dtype=torch.int32, device=dev)
+        self.refs = torch.zeros(num_pages, dtype=torch.int32, device=dev)
+        self.q_offsets: Optional[torch.Tensor] = None
+
+    def _rows(self, rows: Sequence[int]) -> torch.Tensor:
+        return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
+
+    def extend(self, counts: List[int]) -> None:
+        """Room for counts[row] new tokens in each row: sets slots, pos and q_offsets for this step."""
+        offsets = [0]
+        for n in counts:
+            offsets.append(offsets[-1] + int(n))
+        self.q_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
+        r = api.moe_kv_extend(self.q_offsets, offsets[-1], self.table, self.lens, self.refs, self.page_size, inplace=True)
+        self.slots, self.pos = r["slots"], r["pos"]
+
+    def attend(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
+               wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+               interleaved: bool = False, window: int = 0, scale: Optional[float] = None) -> torch.Tensor:
+        """The step's tokens through a layer's attention: norms and rotation of q
+        and k, k and v into the cache, attention of the rotated queries.  q bf16
+        [T, Hq, D], k and v bf16 [T, Hkv, D] in the order of extend()'s counts."""
+        if self.q_offsets is None:
+            raise ValueError("extend() comes before attend()")
+        pool, g_k, g_v = self.pool[layer], self.g_k[layer], self.g_v[layer]
+        q, _ = api.moe_qk_norm_rope(q, k, cos_sin, self.pos, wq=wq, wk=wk, eps=eps, interleaved=interleaved, v=v,
+                                    pool=pool, g_k=g_k, g_v=g_v, slots=self.slots)
+        return api.moe_kv4_attention(q, pool, g_k, g_v, self.q_offsets, self.lens, self.table, scale=scale, window=window)
+
+    def fork(self, src: Sequence[int], dst: Sequence[int]) -> None:
+        """Empty rows dst continue as forks of rows src."""
+        api.moe_kv_fork(self._rows(src), self._rows(dst), self.table, self.lens, self.refs, self.pool, self.page_size,
+                        inplace=True)
+
+    def free(self, rows: Sequence[int]) -> None:
+        api.moe_kv_free(self._rows(rows), self.table, self.lens, self.refs, self.page_size, inplace=True)
+
+    def compact(self) -> torch.Tensor:
+        """Moves the pages in use to the lowest ids; returns the new id of each page (-1: free)."""
+        return api.moe_kv_compact(self.table, self.refs, self.pool, inplace=True)["remap"]
