@@ -495,6 +495,25 @@ def _raw_stream(stream, t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
+# The cache calls run once or more per layer and token, where the host's time is
+# what counts: each looks at its tensors with these predicates (half the cost of
+# the checks that name what is wrong) and falls back to those checks, which
+# raise, only where one of them says no.
+_BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
+
+
+def _is(t, dtype, shape, device: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+
+
+def _is_heads(t, T: int, D: int, device: int) -> bool:
+    if t.dtype is not _BF16 or t.get_device() != device:
+        return False
+    n, h, d = t.shape
+    _, sh, sd = t.stride()
+    return n == T and d == D and sd == 1 and (sh == d or h == 1)
+
+
 def _heads(t: torch.Tensor, name: str, T=None, D=None, device=None) -> None:
     """bf16 [T, heads, D] whose tokens may be apart (a slice of a projection's
     output): heads and D contiguous, any token stride."""
@@ -542,6 +561,50 @@ def moe_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: Optional[torch.T
     [max_pos, rot] with pos int32 [T], or None for no rotation; pool uint8
     [num_pages, Hkv, record] with g_k, g_v fp32 [Hkv] and slots int64 [T].
     Returns (q_out, k_out); k_out is allocated only where there is no pool."""
+    try:
+        T, Hq, D = q.shape
+        di, Hkv, page_bytes = q.get_device(), k.shape[1], 0
+        ok = (di >= 0 and D > 0 and _is_heads(q, T, D, di) and _is_heads(k, T, D, di)
+              and (wq is None or _is(wq, _BF16, (D,), di)) and (wk is None or _is(wk, _BF16, (D,), di)))
+        if ok and cos_sin is not None:
+            max_pos, rot = cos_sin.shape
+            ok = _is(cos_sin, _F32, (max_pos, rot), di) and _is(pos, _I32, (T,), di)
+        if ok and pool is not None:
+            num_pages, _, page_bytes = pool.shape
+            ok = (_is(pool, _U8, (num_pages, Hkv, page_bytes), di) and page_bytes * 8 % (9 * D) == 0
+                  and _is_heads(v, T, D, di) and v.shape[1] == Hkv and _is(g_k, _F32, (Hkv,), di)
+                  and _is(g_v, _F32, (Hkv,), di) and _is(slots, _I64, (T,), di))
+        ok = ok and (q_out is None or _is(q_out, _BF16, (T, Hq, D), di)) and (
+            k_out is None or _is(k_out, _BF16, (T, Hkv, D), di))
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _check_qk_norm_rope(q, k, cos_sin, pos, wq, wk, v, pool, g_k, g_v, slots, q_out, k_out)
+        T, Hq, D = q.shape
+        Hkv, page_bytes = k.shape[1], 0 if pool is None else pool.shape[2]
+    if cos_sin is None:
+        max_pos = rot = 0
+    else:
+        max_pos, rot = cos_sin.shape
+    dev = q.device
+    if q_out is None:
+        q_out = _empty((T, Hq, D), _BF16, dev, stream)
+    if k_out is None and pool is None:
+        k_out = _empty((T, Hkv, D), _BF16, dev, stream)
+    cache = pool is not None
+    check(load().moe_qk_norm_rope(
+        q.data_ptr(), _token_stride(q), k.data_ptr(), _token_stride(k), v.data_ptr() if cache else None,
+        _token_stride(v) if cache else 0, T, Hq, Hkv, D, None if wq is None else wq.data_ptr(),
+        None if wk is None else wk.data_ptr(), eps, None if cos_sin is None else cos_sin.data_ptr(), max_pos, rot,
+        1 if interleaved else 0, None if pos is None else pos.data_ptr(), q_out.data_ptr(),
+        None if k_out is None else k_out.data_ptr(), pool.data_ptr() if cache else None, pool.shape[0] if cache else 0,
+        page_bytes * 8 // (9 * D) if cache else 0, g_k.data_ptr() if cache else None, g_v.data_ptr() if cache else None,
+        slots.data_ptr() if cache else None, _raw_stream(stream, q)), "moe_qk_norm_rope")
+    return q_out, k_out
+
+
+def _check_qk_norm_rope(q, k, cos_sin, pos, wq, wk, v, pool, g_k, g_v, slots, q_out, k_out) -> None:
+    """Raises what is wrong with moe_qk_norm_rope's arguments."""
     _heads(q, "q")
     T, Hq, D = q.shape
     dev = q.device
@@ -549,35 +612,21 @@ def moe_qk_norm_rope(q: torch.Tensor, k: torch.Tensor, cos_sin: Optional[torch.T
     Hkv = k.shape[1]
     _opt(wq, "wq", dtype=torch.bfloat16, shape=(D,), device=dev)
     _opt(wk, "wk", dtype=torch.bfloat16, shape=(D,), device=dev)
-    rot = max_pos = num_pages = page_size = v_stride = 0
     if cos_sin is not None:
         _dev(cos_sin, "cos_sin", dtype=torch.float32, device=dev)
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin: expected [max_pos, rot]")
-        max_pos, rot = cos_sin.shape
         _dev(pos, "pos", dtype=torch.int32, shape=(T,), device=dev)
     if pool is not None:
-        page_size, num_pages = _pool_page_size(pool, Hkv, D, dev), pool.shape[0]
+        _pool_page_size(pool, Hkv, D, dev)
         _heads(v, "v", T, D, dev)
         if v.shape[1] != Hkv:
             raise ValueError(f"v: expected {Hkv} heads, got {v.shape[1]}")
-        v_stride = _token_stride(v)
         _dev(g_k, "g_k", dtype=torch.float32, shape=(Hkv,), device=dev)
         _dev(g_v, "g_v", dtype=torch.float32, shape=(Hkv,), device=dev)
         _dev(slots, "slots", dtype=torch.int64, shape=(T,), device=dev)
-    if q_out is None:
-        q_out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
-    else:
-        _dev(q_out, "q_out", dtype=torch.bfloat16, shape=(T, Hq, D), device=dev)
-    if k_out is None and pool is None:
-        k_out = _empty((T, Hkv, D), torch.bfloat16, dev, stream)
-    elif k_out is not None:
-        _dev(k_out, "k_out", dtype=torch.bfloat16, shape=(T, Hkv, D), device=dev)
-    check(load().moe_qk_norm_rope(_ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), v_stride, T, Hq, Hkv,
-                                  D, _ptr(wq), _ptr(wk), eps, _ptr(cos_sin), max_pos, rot, int(interleaved),
-                                  _ptr(pos), _ptr(q_out), _ptr(k_out), _ptr(pool), num_pages, page_size, _ptr(g_k),
-                                  _ptr(g_v), _ptr(slots), _raw_stream(stream, q)), "moe_qk_norm_rope")
-    return q_out, k_out
+    _opt(q_out, "q_out", dtype=torch.bfloat16, shape=(T, Hq, D), device=dev)
+    _opt(k_out, "k_out", dtype=torch.bfloat16, shape=(T, Hkv, D), device=dev)
 
 
 def moe_kv4_attention(q: torch.Tensor, pool: torch.Tensor, g_k: torch.Tensor, g_v: torch.Tensor,
@@ -590,38 +639,68 @@ def moe_kv4_attention(q: torch.Tensor, pool: torch.Tensor, g_k: torch.Tensor, g_
     [num_pages, Hkv, record], q_offsets int32 [B + 1], kv_lens int32 [B],
     table int32 [B, max_pages]; scale defaults to D ** -0.5; lse fp32 [T, Hq]
     is written where given.  Returns out bf16 [T, Hq, D]."""
+    try:
+        T, Hq, D = q.shape
+        num_pages, Hkv, page_bytes = pool.shape
+        B, max_pages = table.shape
+        di = q.get_device()
+        ok = (di >= 0 and D > 0 and _is_heads(q, T, D, di) and _is(pool, _U8, (num_pages, Hkv, page_bytes), di)
+              and page_bytes * 8 % (9 * D) == 0 and _is(g_k, _F32, (Hkv,), di) and _is(g_v, _F32, (Hkv,), di)
+              and _is(table, _I32, (B, max_pages), di) and _is(q_offsets, _I32, (B + 1,), di)
+              and _is(kv_lens, _I32, (B,), di) and (out is None or _is(out, _BF16, (T, Hq, D), di))
+              and (lse is None or _is(lse, _F32, (T, Hq), di)) and (ws is None or _is(ws, ws.dtype, ws.shape, di)))
+    except (AttributeError, ValueError):
+        ok = False
+    if not ok:
+        _check_kv4_attention(q, pool, g_k, g_v, q_offsets, kv_lens, table, out, lse, ws)
+        T, Hq, D = q.shape
+        num_pages, Hkv, page_bytes = pool.shape
+        B, max_pages = table.shape
+    lib, dev = load(), q.device
+    if out is None:
+        out = _empty((T, Hq, D), _BF16, dev, stream)
+    if ws is None:
+        ws = _empty(lib.moe_kv4_attention_workspace_size(T, B, Hq, Hkv, D), _U8, dev, stream)
+    check(lib.moe_kv4_attention(
+        q.data_ptr(), _token_stride(q), T, Hq, pool.data_ptr(), num_pages, page_bytes * 8 // (9 * D), Hkv, D,
+        g_k.data_ptr(), g_v.data_ptr(), q_offsets.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), B, max_pages,
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, q)),
+        "moe_kv4_attention")
+    return out
+
+
+def _check_kv4_attention(q, pool, g_k, g_v, q_offsets, kv_lens, table, out, lse, ws) -> None:
+    """Raises what is wrong with moe_kv4_attention's arguments."""
     _heads(q, "q")
     T, Hq, D = q.shape
     dev = q.device
     _dev(g_k, "g_k", dtype=torch.float32, device=dev)
     Hkv = g_k.numel()
     _dev(g_v, "g_v", dtype=torch.float32, shape=(Hkv,), device=dev)
-    page_size = _pool_page_size(pool, Hkv, D, dev)
+    _pool_page_size(pool, Hkv, D, dev)
     _dev(table, "table", dtype=torch.int32, device=dev)
     if table.dim() != 2:
         raise ValueError("table: expected [B, max_pages]")
-    B, max_pages = table.shape
+    B = table.shape[0]
     _dev(q_offsets, "q_offsets", dtype=torch.int32, shape=(B + 1,), device=dev)
     _dev(kv_lens, "kv_lens", dtype=torch.int32, shape=(B,), device=dev)
-    if out is None:
-        out = _empty((T, Hq, D), torch.bfloat16, dev, stream)
-    else:
-        _dev(out, "out", dtype=torch.bfloat16, shape=(T, Hq, D), device=dev)
+    _opt(out, "out", dtype=torch.bfloat16, shape=(T, Hq, D), device=dev)
     _opt(lse, "lse", dtype=torch.float32, shape=(T, Hq), device=dev)
-    lib = load()
-    if ws is None:
-        ws = _empty(lib.moe_kv4_attention_workspace_size(T, B, Hq, Hkv, D), torch.uint8, dev, stream)
-    else:
-        _dev(ws, "ws", device=dev)
-    check(lib.moe_kv4_attention(_ptr(q), _token_stride(q), T, Hq, _ptr(pool), pool.shape[0], page_size, Hkv, D,
-                                _ptr(g_k), _ptr(g_v), _ptr(q_offsets), _ptr(kv_lens), _ptr(table), B, max_pages,
-                                D ** -0.5 if scale is None else scale, int(causal), window, _ptr(out), _ptr(lse),
-                                _ptr(ws), ws.numel() * ws.element_size(), _raw_stream(stream, q)), "moe_kv4_attention")
-    return out
+    _opt(ws, "ws", device=dev)
 
 
 def _kv_state(table, refs, lens=None):
     """Checks the arrays of the page operations; returns rows, max_pages, num_pages."""
+    try:
+        S, M = table.shape
+        (N,) = refs.shape
+        di = table.get_device()
+        if (di >= 0 and _is(table, _I32, (S, M), di) and _is(refs, _I32, (N,), di)
+                and (lens is None or _is(lens, _I32, (S,), di))):
+            return S, M, N
+    except (AttributeError, ValueError):
+        pass
     _dev(table, "table", dtype=torch.int32)
     if table.dim() != 2:
         raise ValueError("table: expected [rows, max_pages]")
@@ -640,8 +719,9 @@ def _kv_pools(pool: Optional[torch.Tensor], num_pages: int, device):
     _dev(pool, "pool", dtype=torch.uint8, device=device)
     if pool.dim() < 3 or pool.shape[1] != num_pages:
         raise ValueError(f"pool: expected [layers, {num_pages}, ...], got {tuple(pool.shape)}")
-    page = pool[0, 0].numel() if pool.shape[0] and num_pages else 16
-    return pool.data_ptr(), pool.shape[0], page * num_pages, page
+    layers = pool.shape[0]
+    page = pool.numel() // (layers * num_pages) if layers and num_pages else 16
+    return pool.data_ptr(), layers, page * num_pages, page
 
 
 def _index(t: torch.Tensor, name: str, device) -> int:
@@ -656,7 +736,9 @@ def _like(out, name, t, inplace, stream):
     if out is not None:
         _dev(out, name, dtype=t.dtype, shape=t.shape, device=t.device)
         return out
-    return t if inplace else _empty(t.shape, t.dtype, t.device, stream)
+    if inplace:
+        return t
+    return torch.empty_like(t) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
 
 
 def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
