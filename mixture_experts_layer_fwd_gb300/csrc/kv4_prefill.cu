@@ -74,35 +74,46 @@ DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
-// Half h of a query row to fp16 in the swizzled tile; returns the softmax scale
-// of the row in log2 units (> 0).
+// Half h of a query row to fp16 in the swizzled tile, read in one round trip;
+// the two threads of a row exchange their largest magnitudes.  Returns the
+// softmax scale of the row in log2 units (> 0).
 template <int D>
-DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, int h, uint32_t tile) {
-  const bool have = idx < t.nq * p.G;
-  const int tok = idx / p.G;
-  const uint4* src = reinterpret_cast<const uint4*>(p.q + (t.q0 + tok) * p.q_stride + (t.h * p.G + idx - tok * p.G) * D);
-  uint32_t top = 0;
-  if (have) {
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-      const uint4 v = __ldg(src + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+DEVINL float load_q(const AttnParams& p, const Item& t, int idx, int r, int h, uint32_t tile, float* give,
+                    const float* take, int pair_bar) {
+  constexpr int N = D / 16;  // 16-byte pieces of half a row
+  uint4 v[N];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) top = max(top, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
-    }
+  for (int i = 0; i < N; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  if (idx < t.nq * p.G) {
+    const int tok = idx / p.G;
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + (t.q0 + tok) * p.q_stride + (t.h * p.G + idx - tok * p.G) * D) +
+                       h * N;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __ldg(src + i);
   }
+  const float gk = __ldg(p.g_k + t.h);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) top = max(top, max(w[q] & 0x7FFFu, (w[q] >> 16) & 0x7FFFu));
+  }
+  *give = __uint_as_float(top);
+  named_bar_sync(pair_bar, 64);
+  top = max(top, __float_as_uint(*take));
+  named_bar_sync(pair_bar, 64);  // both have read before either writes again
   float up, sc;
-  row_scale(p.scale * __ldg(p.g_k + t.h), top, up, sc);
-#pragma unroll 2
-  for (int i = h * (D / 16); i < (h + 1) * (D / 16); ++i) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (have) v = __ldg(src + i);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t h[4];
+  row_scale(p.scale * gk, top, up, sc);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint32_t x[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-      h[q] = pack_f16x2(__uint_as_float(w[q] << 16) * up, __uint_as_float(w[q] & 0xFFFF0000u) * up);
-    st_shared_v4(tile + (i >> 3) * Cfg<D>::SUB_Q + r * 128 + (((i & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+      x[q] = pack_f16x2(__uint_as_float(w[q] << 16) * up, __uint_as_float(w[q] & 0xFFFF0000u) * up);
+    const int c = h * N + i;  // piece of the row
+    st_shared_v4(tile + (c >> 3) * Cfg<D>::SUB_Q + r * 128 + (((c & 7) ^ (r & 7)) << 4), x[0], x[1], x[2], x[3]);
   }
   return sc;
 }
@@ -177,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       Item it, nx = items.next(bars.items, tmo, p.err, abort);
       bool end = named_bar_red_or(tile_bar, 256, nx.n == 0);  // all eight leave together
       bool done_one = false;          // `it` holds an item whose output is still in tensor memory
-      float sc = 0.0f;
+      float sc = 0.0f, gv = 0.0f;
       float m = -INFINITY, nb = 0.0f;  // running maximum as used (log2 units); P's shift less it (0 for none)
       uint64_t l2 = 0ull;
       while (true) {
@@ -185,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         const bool mine = !end && nx.rows > g * 128;
         float sc_next = 0.0f;
         if (mine) {
-          sc_next = load_q<D>(p, nx, nx.row0 + g * 128 + r, r, h, sq + g * C::Q_BYTES);
+          sc_next = load_q<D>(p, nx, nx.row0 + g * 128 + r, r, h, sq + g * C::Q_BYTES, give, take, pair_bar);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.qfull[g]);
@@ -203,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           const int tok = idx / p.G;
           const long long row = static_cast<long long>(it.q0 + tok) * p.Hq + it.h * p.G + (idx - tok * p.G);
           const bool whole = it.slot < 0, have = rr < it.rows;
-          const float inv = l > 0.0f ? __ldg(p.g_v + it.h) / l : 0.0f;
+          const float inv = l > 0.0f ? gv / l : 0.0f;
 #pragma unroll 1
           for (int q = 0; q < D / 64; ++q) {
             uint32_t o[32];
@@ -243,6 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         done_one = mine;
         if (mine) {
           sc = sc_next;
+          gv = __ldg(p.g_v + it.h);
           int lo = 0, hi = it.len;  // a row that is not there masks nothing
           if (g * 128 + r < it.rows) item_keys(p, it, it.row0 + g * 128 + r, lo, hi);
           lo -= it.u * kKeys + 64 * h;  // in the thread's 64 keys of the first tile
@@ -515,10 +527,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           // the making: left to themselves they fall into step, and the tensor
           // cores idle while both are in their softmax.
           if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, tmo, p.err, abort);
-          if (mine && nx_first) {
-            wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
-            pq ^= 1;
-          }
           if (cur_mine) {
             wait_warp(&bars.pfull[g], pp, tmo, p.err, abort);
             pp ^= 1;
@@ -535,6 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             umma_commit_warp(&bars.vempty[so]);
           } else if (cur && lane == 0) {
             mbar_arrive(&bars.vempty[so]);
+          }
+          if (mine && nx_first) {  // an item's first tile: its queries
+            wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
+            pq ^= 1;
+            tc_fence_after();
           }
           if (mine) {
             const uint64_t b = dk + st * (C::K_BYTES >> 4);
