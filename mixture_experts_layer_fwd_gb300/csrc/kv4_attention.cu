@@ -115,96 +115,158 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int
 }
 
 // -------------------------------------------------------------------- joining
-// Block (c, y): the item whose first part lies in range c; WARPS warps per row
-// share its parts, rows y * RPB .. of the item.  Parts are added in a fixed
-// order, first those of one warp, then the warps'.
-template <int ROWS, int D, int WARPS>
-__global__ void __launch_bounds__(128) attn_join_kernel(const AttnParams p) {
-  constexpr int RPB = 4 / WARPS;  // rows per block at a time
-  constexpr int V = D / 32;       // columns per lane
+// Block (c, y): the item whose first part lies in range c.  Parts are added in
+// a fixed order, so a call's result is the same each time.
+DEVINL void write_row(const AttnParams& p, const PartItem& t, int r, float m, float l, int D, int lane,
+                      const float* o, int V) {
+  const int idx = t.row0 + r, tok = idx / p.G;
+  const long long row = static_cast<long long>(t.q0 + tok) * p.Hq + t.h * p.G + (idx - tok * p.G);
+  const float inv = l > 0.0f ? __ldg(p.g_v + t.h) / l : 0.0f;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (V / 2);
+#pragma unroll
+  for (int v = 0; v < V / 2; ++v) dst[v] = pack_bf16x2(o[2 * v] * inv, o[2 * v + 1] * inv);
+  if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+}
+
+// Few rows.  With many parts (one context over the whole GPU has a hundred) a
+// block per row, four warps share its parts, eight reads in flight each; with
+// few (a decode batch: two) a warp per row.
+template <int ROWS, int D>
+__global__ void __launch_bounds__(128) attn_join_parts_kernel(const AttnParams p) {
+  constexpr int V = D / 32;  // columns per lane
   __shared__ float s_o[4][D], s_l[4], s_m[4];
   wait_for_previous();
+  const int c = blockIdx.x, r = blockIdx.y;
+  const PartItem t = reinterpret_cast<const PartItem*>(p.part_item)[2 * c + 1];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.0f, o[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) o[v] = 0.0f;
+  if (t.last - c < 4) {
+    const int row = 4 * r + w;
+    if (row >= t.rows) return;
+    float pm[4], pl[4], x[4][V];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = min(c + j, t.last);
+      const long long slot = 2ll * i + (i == c);
+      pm[j] = c + j <= t.last ? p.part_ml[slot * 2 * ROWS + row] : -INFINITY;
+      pl[j] = p.part_ml[(slot * 2 + 1) * ROWS + row];
+      const float* po = p.part_o + (slot * ROWS + row) * D + lane * V;
+#pragma unroll
+      for (int v = 0; v < V; ++v) x[j][v] = po[v];
+    }
+    m = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+    const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float f = ex2(pm[j] - ref);
+      l += f * pl[j];
+#pragma unroll
+      for (int v = 0; v < V; ++v) o[v] += f * x[j][v];
+    }
+    write_row(p, t, row, m, l, D, lane, o, V);
+    return;
+  }
+  if (r >= t.rows) return;
+  for (int base = c + w; base <= t.last; base += 128) {  // lane j: part base + 4 j
+    const int mine = base + 4 * lane;
+    const long long slot = 2ll * mine + (mine == c);
+    float pm = -INFINITY, pl = 0.0f;
+    if (mine <= t.last) {
+      pm = p.part_ml[slot * 2 * ROWS + r];
+      pl = p.part_ml[(slot * 2 + 1) * ROWS + r];
+    }
+    float top = pm;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+    const float mn = fmaxf(m, top);
+    const float ref = mn == -INFINITY ? 0.0f : mn;
+    const float old = ex2(m - ref), f = ex2(pm - ref);
+    float sum = f * pl;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
+    l = l * old + sum;
+    m = mn;
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] *= old;
+    const int n = min(32, (t.last - base) / 4 + 1);
+    for (int j0 = 0; j0 < n; j0 += 8) {
+      float x[8][V];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = base + 4 * min(j0 + j, n - 1);
+        const float* po = p.part_o + ((2ll * i + (i == c)) * ROWS + r) * D + lane * V;
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[j][v] = po[v];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float fj = j0 + j < n ? __shfl_sync(0xFFFFFFFFu, f, j0 + j) : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) o[v] += fj * x[j][v];
+      }
+    }
+  }
+  if (lane == 0) s_m[w] = m, s_l[w] = l;
+#pragma unroll
+  for (int v = 0; v < V; ++v) s_o[w][lane * V + v] = o[v];
+  __syncthreads();
+  if (w != 0) return;
+  const float mx = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  const float ref = mx == -INFINITY ? 0.0f : mx;
+  l = 0.0f;
+#pragma unroll
+  for (int v = 0; v < V; ++v) o[v] = 0.0f;
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const float f = ex2(s_m[x] - ref);
+    l += f * s_l[x];
+#pragma unroll
+    for (int v = 0; v < V; ++v) o[v] += f * s_o[x][lane * V + v];
+  }
+  write_row(p, t, r, mx, l, D, lane, o, V);
+}
+
+// Many rows with few parts: a warp takes four rows side by side.
+template <int ROWS, int D>
+__global__ void __launch_bounds__(128) attn_join_rows_kernel(const AttnParams p) {
+  constexpr int V = D / 32, R = 4;
+  wait_for_previous();
   const int c = blockIdx.x;
-  const PartItem* notes = reinterpret_cast<const PartItem*>(p.part_item);
-  const PartItem t = notes[2 * c + 1];
-  if (t.rows == 0) return;
+  const PartItem t = reinterpret_cast<const PartItem*>(p.part_item)[2 * c + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w = warp % WARPS, sub = warp / WARPS;
-  for (int r0 = blockIdx.y * RPB; r0 < t.rows; r0 += gridDim.y * RPB) {
-    const int r = r0 + sub;
-    const bool have = r < t.rows;
-    float m = -INFINITY, l = 0.0f, o[V];
+  for (int r0 = (blockIdx.y * 4 + warp) * R; r0 < t.rows; r0 += gridDim.y * 4 * R) {
+    float m[R], l[R], o[R][V];
 #pragma unroll
-    for (int v = 0; v < V; ++v) o[v] = 0.0f;
-    if (have) {
-      // lane j looks at parts c + w + WARPS * j, 32 at a time
-      for (int base = c + w; base <= t.last; base += 32 * WARPS) {
-        const int mine = base + WARPS * lane;
-        const long long slot = 2ll * mine + (mine == c);
-        float pm = -INFINITY, pl = 0.0f;
-        if (mine <= t.last) {
-          pm = p.part_ml[slot * 2 * ROWS + r];
-          pl = p.part_ml[(slot * 2 + 1) * ROWS + r];
-        }
-        float top = pm;
+    for (int k = 0; k < R; ++k) {
+      m[k] = -INFINITY, l[k] = 0.0f;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-        const float mn = fmaxf(m, top);
+      for (int v = 0; v < V; ++v) o[k][v] = 0.0f;
+    }
+#pragma unroll 2
+    for (int i = c; i <= t.last; ++i) {
+      const long long slot = 2ll * i + (i == c);
+      const float* ml = p.part_ml + slot * 2 * ROWS + r0;  // rows past t.rows: the item's own padding
+      const float* po = p.part_o + (slot * ROWS + r0) * D + lane * V;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const float pm = ml[k], pl = ml[ROWS + k];
+        float x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = po[k * D + v];
+        const float mn = fmaxf(m[k], pm);
         const float ref = mn == -INFINITY ? 0.0f : mn;
-        const float old = ex2(m - ref);
-        const float f = ex2(pm - ref);
-        float sum = f * pl;
+        const float old = ex2(m[k] - ref), f = ex2(pm - ref);
+        l[k] = l[k] * old + f * pl;
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, x);
-        l = l * old + sum;
-        m = mn;
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] *= old;
-        const int n = min(32, (t.last - base) / WARPS + 1);
-#pragma unroll 4
-        for (int j = 0; j < n; ++j) {
-          const int i = base + WARPS * j;
-          const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
-          const float* po = p.part_o + ((2ll * i + (i == c)) * ROWS + r) * D + lane * V;
-#pragma unroll
-          for (int v = 0; v < V; ++v) o[v] += fj * po[v];
-        }
+        for (int v = 0; v < V; ++v) o[k][v] = o[k][v] * old + f * x[v];
+        m[k] = mn;
       }
     }
-    if (WARPS > 1) {
-      if (lane == 0) s_m[warp] = m, s_l[warp] = l;
 #pragma unroll
-      for (int v = 0; v < V; ++v) s_o[warp][lane * V + v] = o[v];
-      __syncthreads();
-      if (w == 0 && have) {
-        float mx = m;
-#pragma unroll
-        for (int x = 1; x < WARPS; ++x) mx = fmaxf(mx, s_m[warp + x]);
-        const float ref = mx == -INFINITY ? 0.0f : mx;
-        const float f0 = ex2(m - ref);
-        l *= f0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) o[v] *= f0;
-#pragma unroll
-        for (int x = 1; x < WARPS; ++x) {
-          const float f = ex2(s_m[warp + x] - ref);
-          l += f * s_l[warp + x];
-#pragma unroll
-          for (int v = 0; v < V; ++v) o[v] += f * s_o[warp + x][lane * V + v];
-        }
-        m = mx;
-      }
-      __syncthreads();
-    }
-    if (w == 0 && have) {
-      const int idx = t.row0 + r, tok = idx / p.G;
-      const long long row = static_cast<long long>(t.q0 + tok) * p.Hq + t.h * p.G + (idx - tok * p.G);
-      const float inv = l > 0.0f ? __ldg(p.g_v + t.h) / l : 0.0f;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (V / 2);
-#pragma unroll
-      for (int v = 0; v < V / 2; ++v) dst[v] = pack_bf16x2(o[2 * v] * inv, o[2 * v + 1] * inv);
-      if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
-    }
+    for (int k = 0; k < R; ++k)
+      if (r0 + k < t.rows) write_row(p, t, r0 + k, m[k], l[k], D, lane, o[k], V);
   }
 }
 
@@ -610,9 +672,8 @@ int run(const AttnParams& p, int unit, cudaStream_t s) {
   attn_plan_kernel<ROWS><<<1, 1024, 0, s>>>(p, unit);
   MOE_TRY(check_launch());
   MOE_TRY(ROWS == kRows ? launch_rows16<D>(p, s) : attention_tiles(p, D, s));
-  // few rows with many parts, or many rows with few
-  if (ROWS == kRows) return launch_after(attn_join_kernel<ROWS, D, 4>, dim3(p.blocks, 16), 128, 0, s, p);
-  return launch_after(attn_join_kernel<ROWS, D, 1>, dim3(p.blocks, 16), 128, 0, s, p);
+  if constexpr (ROWS == kRows) return launch_after(attn_join_parts_kernel<ROWS, D>, dim3(p.blocks, ROWS), 128, 0, s, p);
+  else return launch_after(attn_join_rows_kernel<ROWS, D>, dim3(p.blocks, ROWS / 16), 128, 0, s, p);
 }
 
 constexpr int kTileRows = kRowsTile, kTileKeys = 128;
