@@ -419,10 +419,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
       const uint8_t* vs = vc + codes_bytes(p.P, D);
       const int key0 = (t.u + i) * p.P;
       const int keys = min(p.P, t.len - key0);
-      wait_warp(&full[st], par, p.timeout_ns, p.err, abort);
+      wait_warp<true>(&full[st], par, p.timeout_ns, p.err, abort);
       if (keys <= 0) {  // a unit without keys
         if (lane == 0) mbar_arrive(&empty[st]);
-        wait_warp(&full[sv], pv, p.timeout_ns, p.err, abort);
+        wait_warp<true>(&full[sv], pv, p.timeout_ns, p.err, abort);
       }
 #pragma unroll 1
       for (int t0 = 0; t0 < keys; t0 += 32) {
@@ -514,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
           }
         }
         if (t0 == 0) {
-          wait_warp(&full[sv], pv, p.timeout_ns, p.err, abort);
+          wait_warp<true>(&full[sv], pv, p.timeout_ns, p.err, abort);
           if (__any_sync(0xFFFFFFFFu, keys < p.P)) {
             // values of keys that were never written: zero scales in the slot,
             // which is the warp's until it hands it back
