@@ -26,9 +26,10 @@ namespace {
 
 constexpr int kRows = kRowsSmall;
 constexpr int kWarps = 4;     // consumer warps of a group
-constexpr int kGroups = 3;    // groups of a block at most, each with its own range of the work
+constexpr int kGroups = 3;    // groups of a block, each with its own range of the work
 constexpr int kThreads = 32 * kGroups * kWarps + 128;  // and a warpgroup with their producers
 constexpr int kMaxSlots = 32;
+constexpr int D = 64;         // of the 16-row kernel here; heads of 128 have kv4_decode.cu's
 constexpr int kSmem = 226 * 1024;
 
 // ------------------------------------------------------------------ schedule
@@ -278,7 +279,6 @@ DEVINL void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // One group's shared memory beside its ring: 4 consumer warps share it.
-template <int D>
 struct Group {
   uint64_t full[kMaxSlots], empty[kMaxSlots];  // warp w's ring: slots w * slots of a warp ..
   ItemRing items;
@@ -287,8 +287,7 @@ struct Group {
   alignas(16) float o[kWarps][kRows][D / 2];  // half the columns at a time
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnParams p, int groups, int slots) {
+__global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnParams p, int slots) {
   constexpr int KS = D / 16;  // k steps of S
   constexpr int LD = D / 4;   // values of a key per lane (S), of a row of O per lane
   constexpr int NT = D / 8;   // column tiles of O
@@ -297,12 +296,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
   const int rec = record_bytes(p.P, D), hb = rec / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int grp = warp < kGroups * kWarps ? warp / kWarps : warp - kGroups * kWarps;
-  constexpr int head = (sizeof(Group<D>) + 127) & ~127;
-  uint8_t* mine = smem + min(grp, groups - 1) * (head + kWarps * slots * hb);
-  Group<D>& sh = *reinterpret_cast<Group<D>*>(mine);
+  constexpr int head = (sizeof(Group) + 127) & ~127;
+  uint8_t* mine = smem + min(grp, kGroups - 1) * (head + kWarps * slots * hb);
+  Group& sh = *reinterpret_cast<Group*>(mine);
   uint8_t* ring = mine + head;
 
-  if (warp < groups * kWarps && warp % kWarps == 0 && lane == 0) {
+  if (warp < kGroups * kWarps && warp % kWarps == 0 && lane == 0) {
     for (int i = 0; i < kMaxSlots; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
@@ -315,15 +314,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
 
   launch_dependents();
   wait_for_previous();
-  const int block = blockIdx.x * groups + grp;  // the group's range
+  const int block = blockIdx.x * kGroups + grp;  // the group's range
   const long long total = total_units(p), range = range_of(p, total);
   const long long x0 = block * range, x1 = min(total, x0 + range);
   int* const abort = &sh.abort;
+  const uint32_t polls = polls_of(p.timeout_ns);
 
   if (warp >= kGroups * kWarps) {
     // -------- one warp per group walks its range and feeds the four warps' rings
     asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (grp >= groups) return;
+    if (grp >= kGroups) return;
     ItemWriter out;
     const int w = lane / slots;  // whose ring; its units of an item are every fourth
     Slot slot;
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
     slot.full = &sh.full[lane], slot.empty = &sh.empty[lane];
     uint32_t it = 0;  // units of the group so far
     walk_range<kRows>(p, p.P, block, x0, x1, range, [&](const Item& t) {
-      out.put(sh.items, t, p.timeout_ns, p.err, abort);
+      out.put(sh.items, t, polls, p.err, abort);
       if (t.n > 0) {
         const int first = (w - static_cast<int>(it)) & (kWarps - 1);
         const int mine = first < t.n ? (t.n - first + kWarps - 1) / kWarps : 0;
@@ -348,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
   }
 
   // -------- consumers: warp w of the group takes the units w, w + 4, ...
-  if (grp >= groups) return;
   asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
   const int wg = warp % kWarps;
   const int g = lane >> 2, c4 = lane & 3;
@@ -359,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
   const uint8_t* my_ring = ring + wg * slots * hb;
   uint64_t *full = sh.full + wg * slots, *empty = sh.empty + wg * slots;
   while (true) {
-    const Item t = items.next(sh.items, p.timeout_ns, p.err, abort);
+    const Item t = items.next(sh.items, polls, p.err, abort);
     if (named_bar_red_or(1 + grp, 32 * kWarps, t.n == 0)) return;  // all four together
     const int n = t.n;
     // rows g and g + 8 of the tile
@@ -419,10 +418,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
       const uint8_t* vs = vc + codes_bytes(p.P, D);
       const int key0 = (t.u + i) * p.P;
       const int keys = min(p.P, t.len - key0);
-      wait_warp<true>(&full[st], par, p.timeout_ns, p.err, abort);
+      wait_warp<true>(&full[st], par, polls, p.err, abort);
       if (keys <= 0) {  // a unit without keys
         if (lane == 0) mbar_arrive(&empty[st]);
-        wait_warp<true>(&full[sv], pv, p.timeout_ns, p.err, abort);
+        wait_warp<true>(&full[sv], pv, polls, p.err, abort);
       }
 #pragma unroll 1
       for (int t0 = 0; t0 < keys; t0 += 32) {
@@ -514,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
           }
         }
         if (t0 == 0) {
-          wait_warp<true>(&full[sv], pv, p.timeout_ns, p.err, abort);
+          wait_warp<true>(&full[sv], pv, polls, p.err, abort);
           if (__any_sync(0xFFFFFFFFu, keys < p.P)) {
             // values of keys that were never written: zero scales in the slot,
             // which is the warp's until it hands it back
@@ -641,29 +640,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
   }
 }
 
-// Groups per block: three, but two where a warp's two half records are 18 KB.
-int groups_of(int P, int D) { return P * D > 64 * 128 ? 2 : kGroups; }
-
-template <int D>
 int launch_rows16(const AttnParams& p, cudaStream_t s) {
   const int half = record_bytes(p.P, D) / 2;
-  const int head = static_cast<int>(round_up(sizeof(Group<D>), 128));
-  const int groups = groups_of(p.P, D);
+  const int head = static_cast<int>(round_up(sizeof(Group), 128));
   // half records per warp: two at least (a unit's keys and values)
-  const int slots = std::min(kMaxSlots / kWarps, (kSmem / groups - head) / (kWarps * half));
-  const int smem = groups * (head + kWarps * slots * half);
+  const int slots = std::min(kMaxSlots / kWarps, (kSmem / kGroups - head) / (kWarps * half));
+  const int smem = kGroups * (head + kWarps * slots * half);
   static bool set[64] = {false};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
   if (!set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_rows16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    const cudaError_t e = cudaFuncSetAttribute(attn_rows16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) {
       set_cuda_error(e);
       return MOE_ERR_CUDA;
     }
     set[dev] = true;
   }
-  return launch_after(attn_rows16_kernel<D>, dim3(p.blocks / groups), kThreads, smem, s, p, groups, slots);
+  return launch_after(attn_rows16_kernel, dim3(p.blocks / kGroups), kThreads, smem, s, p, slots);
 }
 
 // Schedule, main kernel, joining.
@@ -671,7 +665,7 @@ template <int ROWS, int D>
 int run(const AttnParams& p, int unit, cudaStream_t s) {
   attn_plan_kernel<ROWS><<<1, 1024, 0, s>>>(p, unit);
   MOE_TRY(check_launch());
-  MOE_TRY(ROWS == kRows ? launch_rows16<D>(p, s) : attention_tiles(p, D, s));
+  MOE_TRY(ROWS != kRows ? attention_tiles(p, D, s) : D == 128 ? attention_decode(p, s) : launch_rows16(p, s));
   if constexpr (ROWS == kRows) return launch_after(attn_join_parts_kernel<ROWS, D>, dim3(p.blocks, ROWS), 128, 0, s, p);
   else return launch_after(attn_join_rows_kernel<ROWS, D>, dim3(p.blocks, ROWS / 16), 128, 0, s, p);
 }
@@ -689,7 +683,7 @@ Layout layout(AttnParams& p, int D, void* ws) {
   // Up to 32 rows per sequence and kv head on average: 16 rows at a time.
   const bool tiles16 = static_cast<long long>(p.T) * p.G <= 32ll * p.B;
   r.rows = tiles16 ? kRows : kTileRows;
-  r.blocks = tiles16 ? groups_of(p.P, D) * num_sms() : num_sms();
+  r.blocks = tiles16 && D != 128 ? kGroups * num_sms() : num_sms();
   Carve c(ws, 0);
   const long long tiles = static_cast<long long>(p.T) * p.G / r.rows + p.B + 1;
   p.starts = c.take<int>(p.B + 1);
@@ -707,7 +701,7 @@ Layout layout(AttnParams& p, int D, void* ws) {
 }  // namespace
 
 int attention(const AttnParams& p, int D, int rows, cudaStream_t s) {
-  if (rows == kRows) return D == 128 ? run<kRows, 128>(p, p.P, s) : run<kRows, 64>(p, p.P, s);
+  if (rows == kRows) return D == 128 ? run<kRows, 128>(p, kTileKeys, s) : run<kRows, 64>(p, p.P, s);
   return D == 128 ? run<kTileRows, 128>(p, kTileKeys, s) : run<kTileRows, 64>(p, kTileKeys, s);
 }
 
@@ -719,7 +713,7 @@ using namespace moe;
 extern "C" size_t moe_kv4_attention_workspace_size(int T, int B, int Hq, int Hkv, int D) {
   if (T < 1 || B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || !kv4::head_dim_ok(D)) return 0;
   kv4::AttnParams p{};
-  p.T = T, p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.P = 64;  // the most blocks
+  p.T = T, p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv;
   return kv4::layout(p, D, nullptr).bytes;
 }
 

@@ -254,34 +254,35 @@ DEVINL void item_keys(const AttnParams& p, const Item& t, int idx, int& lo, int&
   row_keys(p, s, idx / p.G, lo, hi);
 }
 
-// Bounded wait of a whole warp, every lane testing: mbar_wait_bounded's rules.
-// The test suspends the warp in hardware for a few tens of cycles by itself
-// (given a suspend time it sleeps in steps that cost a round trip each); the
-// clock is read once in 64 tests.  LAZY: for warps that nothing waits for soon.
+// Bounded wait of a whole warp, every lane testing.  The test suspends the warp
+// in hardware for a few tens of cycles by itself (given a suspend time it
+// sleeps in steps that cost a round trip each).  The bound is a number of
+// tests: reading a clock in each of some thirty waits makes a third of the
+// program, which has to stay in the instruction cache.  LAZY: for warps that
+// nothing waits for soon.
 template <bool LAZY = false>
-DEVINL void wait_warp(uint64_t* bar, uint32_t parity, unsigned long long tmo, unsigned int* err, volatile int* abort) {
-  if (!mbar_try_wait(bar, parity)) {
-    uint64_t t0 = 0;
-    for (uint32_t k = 1; !mbar_try_wait(bar, parity); ++k) {
-      if (LAZY) __nanosleep(200);
-      if (k & 63u) continue;
-      const uint64_t now = globaltimer_ns();
-      if (t0 == 0) t0 = now;
-      if (*abort || now - t0 > tmo) {
-        atomicOr(err, kErrTimeout);
-        *abort = 1;
-        break;
-      }
+DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned int* err, volatile int* abort) {
+#pragma unroll 1
+  for (uint32_t k = 0; !mbar_try_wait(bar, parity); ++k) {
+    if (LAZY) __nanosleep(200);
+    if (k == polls) {
+      atomicOr(err, kErrTimeout);
+      *abort = 1;
     }
+    if (*abort) break;
   }
   __syncwarp();
+}
+// Tests in a wait, each some tens of nanoseconds long.
+DEVINL uint32_t polls_of(unsigned long long timeout_ns) {
+  return static_cast<uint32_t>(min(timeout_ns / 32, 0xFFFFFFFFull));
 }
 // One reader's (a warp's) place in an ItemRing.
 struct ItemReader {
   int i = 0;
-  DEVINL Item next(ItemRing& r, unsigned long long tmo, unsigned int* err, volatile int* abort) {
+  DEVINL Item next(ItemRing& r, uint32_t polls, unsigned int* err, volatile int* abort) {
     const int k = i & (kItems - 1);
-    wait_warp(&r.full[k], (i / kItems) & 1, tmo, err, abort);
+    wait_warp(&r.full[k], (i / kItems) & 1, polls, err, abort);
     Item t = r.item[k];
     if (*abort) t.n = 0;
     __syncwarp();
@@ -293,9 +294,9 @@ struct ItemReader {
 // The publishing warp's side (the item is the same in every lane).
 struct ItemWriter {
   int i = 0;
-  DEVINL void put(ItemRing& r, const Item& t, unsigned long long tmo, unsigned int* err, volatile int* abort) {
+  DEVINL void put(ItemRing& r, const Item& t, uint32_t polls, unsigned int* err, volatile int* abort) {
     const int k = i & (kItems - 1);
-    if (i >= kItems) wait_warp<true>(&r.empty[k], (i / kItems - 1) & 1, tmo, err, abort);
+    if (i >= kItems) wait_warp<true>(&r.empty[k], (i / kItems - 1) & 1, polls, err, abort);
     if ((threadIdx.x & 31) == 0) {
       r.item[k] = t;
       mbar_arrive(&r.full[k]);
@@ -450,6 +451,8 @@ DEVINL long long range_of(const AttnParams& p, long long total) {
 
 // Main kernel over 256-row tiles and 128-key units (kv4_prefill.cu).
 int attention_tiles(const AttnParams& p, int D, cudaStream_t s);
+// Main kernel over 16-row tiles and 128-key units, heads of 128 (kv4_decode.cu).
+int attention_decode(const AttnParams& p, cudaStream_t s);
 
 }  // namespace kv4
 }  // namespace moe

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
   uint8_t* ring = smem_raw + C::RING0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = record_bytes(p.P, D) / 2, pages = kKeys / p.P;
-  const unsigned long long tmo = p.timeout_ns;
+  const uint32_t polls = polls_of(p.timeout_ns);
   const int slots[2] = {k_slots, v_slots};
 
   if (threadIdx.x == 0) {
@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       const float* const take = &bars.swap[g][h ^ 1][r];
       uint32_t cnt = 0;  // tiles of keys done
       ItemReader items;
-      Item it, nx = items.next(bars.items, tmo, p.err, abort);
+      Item it, nx = items.next(bars.items, polls, p.err, abort);
       bool end = named_bar_red_or(tile_bar, 256, nx.n == 0);  // all eight leave together
       bool done_one = false;          // `it` holds an item whose output is still in tensor memory
       float sc = 0.0f, gv = 0.0f;
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           unpair(l2, l, lb);
           l += lb;
           *give = l;
-          if (tests) wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
+          if (tests) wait_warp(&bars.ofull[g], (cnt - 1) & 1, polls, p.err, abort);
           named_bar_sync(tile_bar, 256);
           tc_fence_after();
           l = h ? *take + l : l + *take;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           m = -INFINITY, nb = 0.0f;
           l2 = 0ull;
           for (int i = 0; i < it.n; ++i, ++cnt, lo -= kKeys, hi -= kKeys) {
-            if (tests) wait_warp(&bars.sfull[g], cnt & 1, tmo, p.err, abort);
+            if (tests) wait_warp(&bars.sfull[g], cnt & 1, polls, p.err, abort);
             named_bar_sync(tile_bar, 256);
             tc_fence_after();
             if (!__all_sync(0xFFFFFFFFu, lo <= 0 && hi >= 64)) {  // some row does not see all of these keys
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               }
               l2 = fma2(l2, pair(f, f), 0ull);
               if (i > 0) {  // O holds something: bring it to the new maximum
-                wait_warp(&bars.ofull[g], (cnt - 1) & 1, tmo, p.err, abort);
+                wait_warp(&bars.ofull[g], (cnt - 1) & 1, polls, p.err, abort);
                 tc_fence_after();
 #pragma unroll 1
                 for (int q = 0; q < D / 16; ++q) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             if (lane == 0) mbar_arrive(&bars.pfull[g]);
           }
         }
-        nx = items.next(bars.items, tmo, p.err, abort);
+        nx = items.next(bars.items, polls, p.err, abort);
         end = named_bar_red_or(tile_bar, 256, nx.n == 0);
       }
     } else {
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         ItemReader items;
         uint32_t j = 0;
         while (true) {
-          const Item it = items.next(bars.items, tmo, p.err, abort);
+          const Item it = items.next(bars.items, polls, p.err, abort);
           if (named_bar_red_or(team_bar, 128, it.n == 0)) break;  // all four together
           for (int i = 0; i < it.n; ++i, ++j) {
             const uint32_t st = j & 1, ph = (j >> 1) & 1;
@@ -378,11 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               int sl = slot;
               uint32_t rd = round;
               for (int pg = 0; pg < pages; ++pg) {
-                wait_warp(&full[sl], rd, tmo, p.err, abort);
+                wait_warp(&full[sl], rd, polls, p.err, abort);
                 if (++sl == n_slots) sl = 0, rd ^= 1;
               }
             }
-            if (w == 0 && j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, tmo, p.err, abort);
+            if (w == 0 && j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, polls, p.err, abort);
             named_bar_sync(team_bar, 128);
             if (!is_v) {
               // lane = (key, quarter of its values); the warp's keys are 32k + 8w ..
@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         slot.full = &bars.full[v][i], slot.empty = &bars.empty[v][i];
         ItemReader items;
         while (true) {
-          const Item it = items.next(bars.items, tmo, p.err, abort);
+          const Item it = items.next(bars.items, polls, p.err, abort);
           if (it.n == 0) break;
           slot.feed(
               p, it, pages * it.n, half, 2 * half, [&](int k) { return it.u * pages + k; },
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         // ================================================================ walk
         ItemWriter out;
         walk_range<kRows>(p, kKeys, blockIdx.x, x0, x1, range, [&](const Item& t) {
-          out.put(bars.items, t, tmo, p.err, abort);
+          out.put(bars.items, t, polls, p.err, abort);
           return *static_cast<volatile int*>(abort) == 0;
         });
       } else {
@@ -515,20 +515,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         const uint32_t ts = tmem + g * 128, to = tmem + 256 + g * 128;
         uint32_t pq = 0, pp = 0;  // parities of qfull and pfull
         ItemReader items;
-        Item nx = items.next(bars.items, tmo, p.err, abort);
+        Item nx = items.next(bars.items, polls, p.err, abort);
         int rem = nx.n;
         bool nx_first = true, cur = false, cur_mine = false, cur_first = false;
         for (uint32_t j = 0; rem > 0 || cur; ++j) {
           const uint32_t st = j & 1, so = st ^ 1;
           const bool more = rem > 0, mine = more && nx.rows > g * 128;
-          if (more) wait_warp(&bars.kfull[st], (j >> 1) & 1, tmo, p.err, abort);
-          if (cur) wait_warp(&bars.vfull[so], ((j - 1) >> 1) & 1, tmo, p.err, abort);
+          if (more) wait_warp(&bars.kfull[st], (j >> 1) & 1, polls, p.err, abort);
+          if (cur) wait_warp(&bars.vfull[so], ((j - 1) >> 1) & 1, polls, p.err, abort);
           // The tiles take turns, one's products queued while the other's S is in
           // the making: left to themselves they fall into step, and the tensor
           // cores idle while both are in their softmax.
-          if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, tmo, p.err, abort);
+          if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, polls, p.err, abort);
           if (cur_mine) {
-            wait_warp(&bars.pfull[g], pp, tmo, p.err, abort);
+            wait_warp(&bars.pfull[g], pp, polls, p.err, abort);
             pp ^= 1;
           }
           tc_fence_after();
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             mbar_arrive(&bars.vempty[so]);
           }
           if (mine && nx_first) {  // an item's first tile: its queries
-            wait_warp(&bars.qfull[g], pq, tmo, p.err, abort);
+            wait_warp(&bars.qfull[g], pq, polls, p.err, abort);
             pq ^= 1;
             tc_fence_after();
           }
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           cur = more, cur_mine = mine, cur_first = nx_first;
           nx_first = false;
           if (more && --rem == 0) {
-            nx = items.next(bars.items, tmo, p.err, abort);
+            nx = items.next(bars.items, polls, p.err, abort);
             rem = nx.n;
             nx_first = true;
           }
