@@ -680,8 +680,12 @@ struct Layout {
 // Kernel variant, its blocks, and the workspace they need; fills p's pointers.
 Layout layout(AttnParams& p, int D, void* ws) {
   Layout r;
-  // Up to 32 rows per sequence and kv head on average: 16 rows at a time.
-  const bool tiles16 = static_cast<long long>(p.T) * p.G <= 32ll * p.B;
+  // Rows per sequence and kv head on average: the 16-row kernels expand the
+  // cache's codes again for every 16 rows, the 256-row kernel once, at the price
+  // of products 256 rows wide.  64 sequences of 8192 keys, 4 kv heads of 128, 16 /
+  // 32 / 48 / 64 rows: 85 / 151 / 217 / 282 us against 239 / 241 / 241 / 242;
+  // of 64: 68 / 112 / 160 / 203 against 176 / 176 / 177 / 177.
+  const bool tiles16 = static_cast<long long>(p.T) * p.G <= 48ll * p.B;
   r.rows = tiles16 ? kRows : kTileRows;
   r.blocks = tiles16 && D != 128 ? kGroups * num_sms() : num_sms();
   Carve c(ws, 0);
