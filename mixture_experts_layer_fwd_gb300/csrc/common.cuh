@@ -530,6 +530,14 @@ DEVINL uint64_t smem_desc_kmajor_sw128(uint32_t saddr) {
   return d;
 }
 
+// The same for an operand that lies with its rows (of M or N) contiguous, 64 of
+// them per 128-byte line: 8 lines (of K) make 1024 bytes, the next 64 rows come
+// `next` bytes further.  The instruction descriptor says so by kMajorA, kMajorB.
+DEVINL uint64_t smem_desc_mnmajor_sw128(uint32_t saddr, uint32_t next) {
+  return (smem_desc_kmajor_sw128(saddr) & ~(0x3FFFull << 16)) | static_cast<uint64_t>(next >> 4) << 16;
+}
+constexpr uint32_t kMajorA = 1u << 15, kMajorB = 1u << 16;
+
 // Shared-memory descriptor of a K-major operand without swizzle whose rows
 // are 16 bytes, stored contiguously (8-row core matrices 128 bytes apart):
 // the layout of a 32 x 128-bit block of scale factors for tcgen05.cp.

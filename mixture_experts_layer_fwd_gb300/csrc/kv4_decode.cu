@@ -125,13 +125,6 @@ DEVINL void tmem_st_16x256b_x4(uint32_t addr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-// A tile with its rows (M) contiguous in memory, 64 of them per 128-byte line
-// with 128-byte swizzle: 8 lines of K make 1024 bytes, the next 64 rows come
-// SUB_V bytes further.
-DEVINL uint64_t smem_desc_mmajor_sw128(uint32_t addr) {
-  return (smem_desc_kmajor_sw128(addr) & ~(0x3FFFull << 16)) | static_cast<uint64_t>(SUB_V >> 4) << 16;
-}
-constexpr uint32_t kMMajorA = 1u << 15;  // of the instruction descriptor
 // Four 8 x 8 matrices of 16-bit values, transposed on the way; lane 8 i + k
 // gives the address of row k of the i-th in shared memory.
 DEVINL void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
@@ -631,13 +624,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
           } else {  // O^T += V^T P^T
             wait_warp(&bars.vready[vs], vround & 1, polls, p.err, abort);
             tc_fence_after();
-            const uint64_t a = smem_desc_mmajor_sw128(base + vs % kVStages * V_BYTES);
+            const uint64_t a = smem_desc_mnmajor_sw128(base + vs % kVStages * V_BYTES, SUB_V);
             const uint64_t b = smem_desc_kmajor_sw128(base + P0 + buf * P_BYTES);
             if (elect_one()) {
 #pragma unroll
               for (int kk = 0; kk < kKeys / 16; ++kk)
                 umma_f16(tmem + O0 + (2 * (seq & 1) + (buf >> 1)) * kRows, a + kk * (16 * 128 >> 4), b + (kk >> 2) * (SUB_Q >> 4) + (kk & 3) * 2,
-                         idesc_f16_f32(128, kRows) | kMMajorA, (i & ~2) || kk ? 1u : 0u);
+                         idesc_f16_f32(128, kRows) | kMajorA, (i & ~2) || kk ? 1u : 0u);
               umma_commit(&bars.vdone[vs]);
             }
             if (++vs == kVSteps) vs = 0, ++vround;

@@ -41,8 +41,7 @@ template <int D>
 struct Cfg {
   static constexpr int Q_BYTES = 128 * D * 2;     // one row tile
   static constexpr int K_BYTES = kKeys * D * 2;   // one tile of keys; V the same
-  static constexpr int SUB_Q = 128 * 128;         // 64-wide sub-tile of Q or K
-  static constexpr int SUB_V = D * 128;           // 64-key sub-tile of V transposed
+  static constexpr int SUB_Q = 128 * 128;         // 64-wide sub-tile of Q, K or V
   static constexpr int BARS0 = 2 * Q_BYTES + 4 * K_BYTES;
   static constexpr int RING0 = BARS0 + 3328;
   static constexpr int RING = (D == 128 ? 227 : 160) * 1024 - RING0;
@@ -352,9 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         const bool is_v = warp >= kExpandV;
         const int w = warp & 3, c4 = lane & 3;
         const int team_bar = is_v ? 12 : 11;  // warp 0 tests barriers for the four
-        const int tg = lane & 7, tgh = w & 1;  // V: group of 8 keys in a 64-key sub-tile
-        const int blk = D == 128 ? (2 * (tg >> 1) + (lane >> 3) + 4 * (w >> 1)) & 7 : (2 * (tg >> 1) + (lane >> 3)) & 3;
-        const int odd = tg & 1;
         const int logp = p.P == 32 ? 5 : p.P == 64 ? 6 : 7;
         const int n_slots = is_v ? v_slots : k_slots;
         const uint8_t* my_ring = ring + (is_v ? k_slots * half : 0);
@@ -384,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             }
             if (w == 0 && j >= 2) wait_warp(is_v ? &bars.vempty[st] : &bars.kempty[st], ph ^ 1, polls, p.err, abort);
             named_bar_sync(team_bar, 128);
-            if (!is_v) {
-              // lane = (key, quarter of its values); the warp's keys are 32k + 8w ..
-              constexpr int W = D / 32;  // words of 8 codes per lane
-              const bool hi = W == 4 && (c4 & 2);
-              const int key0 = 8 * w + (lane >> 2);
+            // lane = (key, quarter of its values); the warp's keys are 32k + 8w ..
+            constexpr int W = D / 32;  // words of 8 codes per lane
+            const bool hi = W == 4 && (c4 & 2);
+            const int key0 = 8 * w + (lane >> 2);
+            const int keys = it.len - (it.u + i) * kKeys;  // past them the bytes are not a key's
 #pragma unroll 1
-             for (int k2 = 0; k2 < 4; k2 += 2) {
+            for (int k2 = 0; k2 < 4; k2 += 2) {
               uint32_t cw[2][W], sb[2];
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
@@ -406,10 +402,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                   sb[k] = kc[codes_bytes(p.P, D) + in * (D / 16) + c4];
                 }
               }
-              const uint32_t row = sk + st * C::K_BYTES + (W == 4 ? (c4 >> 1) * C::SUB_Q : 0) + (32 * k2 + key0) * 128;
+              const uint32_t row =
+                  (is_v ? sv : sk) + st * C::K_BYTES + (W == 4 ? (c4 >> 1) * C::SUB_Q : 0) + (32 * k2 + key0) * 128;
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const uint32_t f = e4m3x2_to_f16x2(sb[k]);
+                const uint32_t f = e4m3x2_to_f16x2(32 * (k2 + k) + key0 < keys ? sb[k] : 0u);
                 // lanes 2, 3 of a key write their chunks in another order: no two of a phase on the same banks
                 const uint32_t f0 = __byte_perm(f, f, hi ? 0x3232 : 0x1010), f1 = __byte_perm(f, f, hi ? 0x1010 : 0x3232);
 #pragma unroll
@@ -420,51 +417,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                   const uint32_t fq = W == 4 && q >= 2 ? f1 : f0;
                   st_shared_v4(row + k * 32 * 128 + ((chunk ^ (key0 & 7)) << 4), hmul2(h[0], fq), hmul2(h[1], fq),
                                hmul2(h[2], fq), hmul2(h[3], fq));
-                }
-              }
-             }
-            } else if (D == 128 || w < 2) {
-              // thread = (8 keys, block of 16 values)
-              const int first = tgh * 64 + tg * 8;
-              const int in = first & (p.P - 1);
-              const uint8_t* vc = my_ring + half_of(first) + in * (D / 2) + 8 * blk;
-              const uint8_t* vs = my_ring + half_of(first) + codes_bytes(p.P, D) + in * (D / 16) + blk;
-              // register q holds key q ^ odd, so that neighbours read different banks
-              const uint8_t *vc0 = vc + odd * (D / 2), *vc1 = vc - odd * (D / 2);
-              uint2 cw[8];
-              uint32_t sb[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                cw[q] = *reinterpret_cast<const uint2*>((q & 1 ? vc1 : vc0) + q * (D / 2));
-                sb[q] = vs[q * (D / 16)];
-              }
-              const int keys = it.len - (it.u + i) * kKeys - first;  // of the 8 that were written
-              if (keys < 8) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                  if (q >= keys) sb[q] = 0u;
-              }
-              uint32_t f[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q) f[q] = e4m3x2_to_f16x2(sb[2 * q] | (sb[2 * q + 1] << 8));
-              const uint32_t vt = sv + st * C::K_BYTES + tgh * C::SUB_V + 16 * blk * 128;
-#pragma unroll
-              for (int v = 0; v < 4; ++v) {  // word v / 2, even or odd values
-                uint32_t h[4][4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  const uint32_t x = v >> 1 ? cw[2 * q].y : cw[2 * q].x, y = v >> 1 ? cw[2 * q + 1].y : cw[2 * q + 1].x;
-                  const uint32_t a = odd ? y : x, b = odd ? x : y;
-                  uint32_t e[4];
-                  e2m1x8(v & 1 ? ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u)
-                               : (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), e);
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) h[k][q] = hmul2(e[k], f[q]);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const int d = 2 * k + (v & 1);  // in the word
-                  st_shared_v4(vt + (8 * (v >> 1) + d) * 128 + ((tg ^ d) << 4), h[k][0], h[k][1], h[k][2], h[k][3]);
                 }
               }
             }
@@ -511,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         // O_g += P_g V(j - 1) and S_g = Q_g K(j)^T back to back.
         const int g = warp - kMma;
         const uint64_t dq = smem_desc_kmajor_sw128(sq + g * C::Q_BYTES);
-        const uint64_t dk = smem_desc_kmajor_sw128(sk), dv = smem_desc_kmajor_sw128(sv);
+        const uint64_t dk = smem_desc_kmajor_sw128(sk), dv = smem_desc_mnmajor_sw128(sv, C::SUB_Q);
         const uint32_t ts = tmem + g * 128, to = tmem + 256 + g * 128;
         uint32_t pq = 0, pp = 0;  // parities of qfull and pfull
         ItemReader items;
@@ -536,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
             const uint64_t b = dv + so * (C::K_BYTES >> 4);
 #pragma unroll
             for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + (kk >> 2) * (C::SUB_V >> 4) + (kk & 3) * 2, idesc_f16_f32(128, D),
+              umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4), idesc_f16_f32(128, D) | kMajorB,
                                cur_first && kk == 0 ? 0u : 1u);
             umma_commit_warp(&bars.ofull[g]);
             umma_commit_warp(&bars.turn[g ^ 1]);
