@@ -8,6 +8,12 @@
 // binary tree over neighbours, so a token's results, down to the cache's
 // bytes, do not depend on the batch it came in or on the launch shape, and
 // equal the elementary formula's bit for bit.
+//
+// Bound: HBM for many tokens.  16384 tokens of 64 + 4 heads of 128: 129 us, 4.6
+// TB/s (0.67 of a copy), with 59 % of the issue slots taken; plain fp32
+// instructions 175 us, packed pairs with four inverse roots side by side 129;
+// 64 registers 132 us, 48 157, the next loads in flight during a step 129.  One
+// token: 6 us, latency.
 #include "kv4.cuh"
 
 namespace moe {
