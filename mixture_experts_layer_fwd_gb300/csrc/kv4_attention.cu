@@ -40,8 +40,10 @@ constexpr int D = 64;         // of the 16-row kernel here; heads of 128 have kv
 constexpr int kSmem = 226 * 1024;
 
 // ------------------------------------------------------------------ schedule
-template <int ROWS>
-__global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int unit) {
+// One block; of a warp where a warp has a lane for every sequence and tile (no
+// block-wide steps), else of 1024 threads.
+template <int ROWS, int THREADS>
+__global__ void __launch_bounds__(THREADS) attn_plan_kernel(const AttnParams p, int unit) {
   __shared__ long long s_warp[32];
   launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -51,6 +53,11 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int
     for (int o = 1; o < 32; o <<= 1) {
       const long long up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
       if (lane >= o) incl += up;
+    }
+    if (THREADS == 32) {
+      __syncwarp();
+      total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      return incl - v;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
@@ -72,7 +79,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int
   // running maximum of the offsets: whatever they hold, the rows of all
   // sequences are disjoint and inside q, so the tiles fit the workspace
   int before_all = 0;
-  for (int base = 0; base <= p.B; base += 1024) {
+  for (int base = 0; base <= p.B; base += THREADS) {
     const int b = base + threadIdx.x;
     int v = b <= p.B ? min(max(p.q_offsets[b], 0), p.T) : 0;
 #pragma unroll
@@ -80,16 +87,24 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int
       const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
       if (lane >= o) v = max(v, up);
     }
-    if (lane == 31) s_warp[warp] = v;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) v = max(v, static_cast<int>(s_warp[w]));
-    v = max(v, before_all);
+    if (THREADS > 32) {
+      if (lane == 31) s_warp[warp] = v;
+      __syncthreads();
+      // lane w: what warp w reached
+      int all = static_cast<int>(s_warp[lane]), mine = lane < warp ? all : 0;
+      mine = __reduce_max_sync(0xFFFFFFFFu, mine);
+      all = __reduce_max_sync(0xFFFFFFFFu, all);
+      v = max(max(v, mine), before_all);
+      before_all = max(before_all, all);
+    } else {
+      v = max(v, before_all);
+      before_all = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
     if (b <= p.B) p.starts[b] = v;
-    for (int w = 0; w < 32; ++w) before_all = max(before_all, static_cast<int>(s_warp[w]));
     __syncthreads();
   }
   long long tiles = 0;
-  for (int base = 0; base < p.B; base += 1024) {
+  for (int base = 0; base < p.B; base += THREADS) {
     const int b = base + threadIdx.x;
     long long n = 0, total;
     if (b < p.B) n = (static_cast<long long>(load_seq(p, b).n) * p.G + ROWS - 1) / ROWS;
@@ -100,7 +115,7 @@ __global__ void __launch_bounds__(1024) attn_plan_kernel(const AttnParams p, int
   if (threadIdx.x == 0) p.tile_base[p.B] = static_cast<int>(tiles);
   __syncthreads();
   long long units = 0;
-  for (long long base = 0; base < tiles; base += 1024) {
+  for (long long base = 0; base < tiles; base += THREADS) {
     const long long f = base + threadIdx.x;
     long long n = 0, total;
     if (f < tiles) {
@@ -670,7 +685,8 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
 // Schedule, main kernel, joining.
 template <int ROWS, int D>
 int run(const AttnParams& p, int unit, cudaStream_t s) {
-  attn_plan_kernel<ROWS><<<1, 1024, 0, s>>>(p, unit);
+  if (p.B < 32 && static_cast<long long>(p.T) * p.G / ROWS + p.B <= 32) attn_plan_kernel<ROWS, 32><<<1, 32, 0, s>>>(p, unit);
+  else attn_plan_kernel<ROWS, 1024><<<1, 1024, 0, s>>>(p, unit);
   MOE_TRY(check_launch());
   MOE_TRY(ROWS != kRows ? attention_tiles(p, D, s) : D == 128 ? attention_decode(p, s) : launch_rows16(p, s));
   if constexpr (ROWS == kRows) return launch_after(attn_join_parts_kernel<ROWS, D>, dim3(p.blocks, ROWS), 128, 0, s, p);
