@@ -24,12 +24,13 @@
 // Numbers are as in the 16-row kernel: codes times block scales and Q times a
 // power of two are exact in fp16, P is rounded to fp16, sums are fp32.
 //
-// 4096 queries on 12289 keys, 64 heads on 4 of 128: 1.06 ms, 1.30 PFLOP/s; the
+// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.98 ms, 1.41 PFLOP/s; the
 // same with heads of 64 0.88 ms.  What bounds it is the chain scores, softmax,
 // weights, next scores of a tile, since scores and weights share columns.  Half
 // a row per thread 1.17 against 1.21 ms, one tester of a barrier for the eight
 // warps of a tile 1.09 against 1.13, walking the items in a warp of its own
-// (half the code) 1.39 against 2.12.
+// (half the code) 1.39 against 2.12; with heads of 64 P has room beside S, but
+// without turns the tiles fall into step: 1.02 against 0.88.
 #include "kv4_attention.cuh"
 
 namespace moe {
@@ -485,39 +486,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           // the making: left to themselves they fall into step, and the tensor
           // cores idle while both are in their softmax.
           if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, polls, p.err, abort);
-          if (cur_mine) {
-            wait_warp(&bars.pfull[g], pp, polls, p.err, abort);
-            pp ^= 1;
-          }
-          tc_fence_after();
-          if (cur_mine) {
-            const uint64_t b = dv + so * (C::K_BYTES >> 4);
+          // O += P V, then S = Q K^T, which P lies over.  A rolled loop keeps what
+          // S needs out of the way of P's product: 0.98 against 1.05 ms unrolled.
+#pragma unroll 1
+          for (int step = 0; step < 2; ++step) {
+            if (step == 0) {
+              if (cur_mine) {
+                wait_warp(&bars.pfull[g], pp, polls, p.err, abort);
+                pp ^= 1;
+                tc_fence_after();
+                const uint64_t b = dv + so * (C::K_BYTES >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4), idesc_f16_f32(128, D) | kMajorB,
-                               cur_first && kk == 0 ? 0u : 1u);
-            umma_commit_warp(&bars.ofull[g]);
-            umma_commit_warp(&bars.turn[g ^ 1]);
-            umma_commit_warp(&bars.vempty[so]);
-          } else if (cur && lane == 0) {
-            mbar_arrive(&bars.vempty[so]);
-          }
-          if (mine && nx_first) {  // an item's first tile: its queries
-            wait_warp(&bars.qfull[g], pq, polls, p.err, abort);
-            pq ^= 1;
-            tc_fence_after();
-          }
-          if (mine) {
-            const uint64_t b = dk + st * (C::K_BYTES >> 4);
+                for (int kk = 0; kk < kKeys / 16; ++kk)
+                  umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4),
+                                   idesc_f16_f32(128, D) | kMajorB, cur_first && kk == 0 ? 0u : 1u);
+                umma_commit_warp(&bars.ofull[g]);
+                umma_commit_warp(&bars.turn[g ^ 1]);
+                umma_commit_warp(&bars.vempty[so]);
+              } else if (cur && lane == 0) {
+                mbar_arrive(&bars.vempty[so]);
+              }
+            } else if (mine) {
+              if (nx_first) {  // an item's first tile: its queries
+                wait_warp(&bars.qfull[g], pq, polls, p.err, abort);
+                pq ^= 1;
+              }
+              tc_fence_after();
+              const uint64_t b = dk + st * (C::K_BYTES >> 4);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
-              umma_f16_ss_warp(ts, dq + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
+                umma_f16_ss_warp(ts, dq + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
+              }
+              umma_commit_warp(&bars.sfull[g]);
+              umma_commit_warp(&bars.kempty[st]);
+            } else if (more && lane == 0) {
+              mbar_arrive(&bars.kempty[st]);
             }
-            umma_commit_warp(&bars.sfull[g]);
-            umma_commit_warp(&bars.kempty[st]);
-          } else if (more && lane == 0) {
-            mbar_arrive(&bars.kempty[st]);
           }
           if (!cur_mine && lane == 0) mbar_arrive(&bars.turn[g ^ 1]);
           __syncwarp();
