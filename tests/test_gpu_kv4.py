@@ -227,6 +227,34 @@ def test_attention_of_rising_scores(qs):
     check_attention(c, 64, 0.2)
 
 
+@pytest.mark.parametrize("qs", [[1, 2], [60, 80]])
+@pytest.mark.parametrize("kvs", [[1500, 640], [1408, 129]])
+def test_attention_of_rising_scores_on_long_contexts(qs, kvs):
+    """Heads of 128: every pair of tiles moves the maximum; odd and even numbers of tiles."""
+    c = attn_case(128, 1, 2, 64, qs, kvs, seed=16)
+    for b in range(2):
+        for j in range(-(-kvs[b] // 64)):
+            oa.sections(c["pool"][c["table"][b, j], 0], 64, 128)[1][:] = 0x30 + j
+    check_attention(c, 64, 0.1)
+
+
+@pytest.mark.parametrize("D,P,window", [(128, 64, 0), (128, 32, 100), (128, 128, 0), (64, 64, 0)])
+def test_attention_of_many_short_sequences(D, P, window):
+    """Several items per block, of any number of tiles, some of them shared by two blocks, some rows empty."""
+    rng = np.random.default_rng(D + P)
+    qs = [int(n) for n in rng.integers(0, 3, 330)]
+    kvs = [int(n) for n in rng.integers(0, 400, 330)]
+    kvs[7], qs[7], kvs[200], qs[200] = 3000, 1, 0, 2
+    check_attention(attn_case(D, 2, 2, P, qs, kvs, seed=17), P, D ** -0.5, window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [2, 3, 4])
+def test_attention_of_few_tokens_of_many_heads(D, n):
+    """32, 48 and 64 rows per sequence and kv head, on either side of the kernels' border."""
+    check_attention(attn_case(D, 1, 16, 64, [n] * 3, [n, 70, 391], seed=18), 64, D ** -0.5)
+
+
 @pytest.mark.parametrize("qs", [[1, 2, 1], [50, 1, 99]])
 def test_attention_queries_are_slices_on_another_stream(qs):
     c = attn_case(128, 1, 4, 64, qs, [200, 130, 99], seed=13)
