@@ -46,95 +46,7 @@ template <int ROWS, int THREADS>
 __global__ void __launch_bounds__(THREADS) attn_plan_kernel(const AttnParams p, int unit) {
   __shared__ long long s_warp[32];
   launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto scan = [&](long long v, long long& total) {
-    long long incl = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += up;
-    }
-    if (THREADS == 32) {
-      __syncwarp();
-      total = __shfl_sync(0xFFFFFFFFu, incl, 31);
-      return incl - v;
-    }
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    if (warp == 0) {
-      long long w = s_warp[lane];
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long up = __shfl_up_sync(0xFFFFFFFFu, w, o);
-        if (lane >= o) w += up;
-      }
-      s_warp[lane] = w;
-    }
-    __syncthreads();
-    const long long before = warp ? s_warp[warp - 1] : 0;
-    total = s_warp[31];
-    __syncthreads();
-    return before + incl - v;
-  };
-  // running maximum of the offsets: whatever they hold, the rows of all
-  // sequences are disjoint and inside q, so the tiles fit the workspace
-  int before_all = 0;
-  for (int base = 0; base <= p.B; base += THREADS) {
-    const int b = base + threadIdx.x;
-    int v = b <= p.B ? min(max(p.q_offsets[b], 0), p.T) : 0;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
-      if (lane >= o) v = max(v, up);
-    }
-    if (THREADS > 32) {
-      if (lane == 31) s_warp[warp] = v;
-      __syncthreads();
-      // lane w: what warp w reached
-      int all = static_cast<int>(s_warp[lane]), mine = lane < warp ? all : 0;
-      mine = __reduce_max_sync(0xFFFFFFFFu, mine);
-      all = __reduce_max_sync(0xFFFFFFFFu, all);
-      v = max(max(v, mine), before_all);
-      before_all = max(before_all, all);
-    } else {
-      v = max(v, before_all);
-      before_all = __shfl_sync(0xFFFFFFFFu, v, 31);
-    }
-    if (b <= p.B) p.starts[b] = v;
-    __syncthreads();
-  }
-  long long tiles = 0;
-  for (int base = 0; base < p.B; base += THREADS) {
-    const int b = base + threadIdx.x;
-    long long n = 0, total;
-    if (b < p.B) n = (static_cast<long long>(load_seq(p, b).n) * p.G + ROWS - 1) / ROWS;
-    const long long at = scan(n, total);
-    if (b < p.B) p.tile_base[b] = static_cast<int>(tiles + at);
-    tiles += total;
-  }
-  if (threadIdx.x == 0) p.tile_base[p.B] = static_cast<int>(tiles);
-  __syncthreads();
-  long long units = 0;
-  for (long long base = 0; base < tiles; base += THREADS) {
-    const long long f = base + threadIdx.x;
-    long long n = 0, total;
-    if (f < tiles) {
-      int lo = 0, hi = p.B;  // largest b with tile_base[b] <= f
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.tile_base[mid] <= f) lo = mid;
-        else hi = mid;
-      }
-      const Seq s = load_seq(p, lo);
-      int u0, u1;
-      tile_units<ROWS>(p, s, static_cast<int>(f - p.tile_base[lo]), unit, u0, u1);
-      n = u1 - u0;
-    }
-    const long long at = scan(n, total);
-    if (f < tiles) p.unit_sum[f] = units + at;
-    units += total;
-  }
-  if (threadIdx.x == 0) p.unit_sum[tiles] = units;
+  plan<ROWS, THREADS>(p, unit, s_warp);
 }
 
 // -------------------------------------------------------------------- joining
@@ -685,9 +597,11 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
 // Schedule, main kernel, joining.
 template <int ROWS, int D>
 int run(const AttnParams& p, int unit, cudaStream_t s) {
-  if (p.B < 32 && static_cast<long long>(p.T) * p.G / ROWS + p.B <= 32) attn_plan_kernel<ROWS, 32><<<1, 32, 0, s>>>(p, unit);
-  else attn_plan_kernel<ROWS, 1024><<<1, 1024, 0, s>>>(p, unit);
-  MOE_TRY(check_launch());
+  if (!p.plan_here) {
+    if (p.B < 32 && static_cast<long long>(p.T) * p.G / ROWS + p.B <= 32) attn_plan_kernel<ROWS, 32><<<1, 32, 0, s>>>(p, unit);
+    else attn_plan_kernel<ROWS, 1024><<<1, 1024, 0, s>>>(p, unit);
+    MOE_TRY(check_launch());
+  }
   MOE_TRY(ROWS != kRows ? attention_tiles(p, D, s) : D == 128 ? attention_decode(p, s) : launch_rows16(p, s));
   if constexpr (ROWS == kRows) return launch_after(attn_join_parts_kernel<ROWS, D>, dim3(p.blocks, ROWS), 128, 0, s, p);
   else return launch_after(attn_join_rows_kernel<ROWS, D>, dim3(p.blocks, ROWS / 16), 128, 0, s, p);
@@ -721,6 +635,8 @@ Layout layout(AttnParams& p, int D, void* ws) {
   p.part_o = c.take<float>(static_cast<size_t>(2) * r.blocks * r.rows * D);
   p.blocks = r.blocks;
   p.min_units = tiles16 ? 1 : 2;
+  // a launch less for few sequences: one query 22 against 28 us with the call's host time
+  p.plan_here = tiles16 && D == 128 && p.B <= kPlanHere && static_cast<long long>(p.T) * p.G / r.rows + p.B <= kPlanHere;
   r.bytes = c.used;
   return r;
 }

@@ -100,6 +100,7 @@ struct AttnParams {
   long long* unit_sum;  // [tiles + 1] units of one kv head before row tile f
   int blocks;           // ranges: blocks of the main kernel, or groups of its warps
   int min_units;        // least units of a block's range
+  int plan_here;        // every block of the main kernel makes the schedule for itself
   int *part_item;  // [2 * blocks][8]: what a slot holds (PartItem)
   // partial results: slot 2 * block (the item begun by an earlier block) and 2 * block + 1
   float *part_o, *part_ml;  // [2 * blocks][ROWS][D], [2 * blocks][2][ROWS]
@@ -443,6 +444,105 @@ inline int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int s
   return MOE_OK;
 }
 
+// The schedule (starts, tile_base, unit_sum) by a warp or a block of 1024
+// threads, which shares the 32 words s_warp.
+template <int ROWS, int THREADS>
+DEVINL void plan(const AttnParams& p, int unit, long long* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tid = THREADS == 32 ? lane : threadIdx.x;
+  auto sync = [] {
+    if (THREADS == 32) __syncwarp();
+    else __syncthreads();
+  };
+  auto scan = [&](long long v, long long& total) {
+    long long incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += up;
+    }
+    if (THREADS == 32) {
+      __syncwarp();
+      total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+      return incl - v;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    sync();
+    if (warp == 0) {
+      long long w = s_warp[lane];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xFFFFFFFFu, w, o);
+        if (lane >= o) w += up;
+      }
+      s_warp[lane] = w;
+    }
+    sync();
+    const long long before = warp ? s_warp[warp - 1] : 0;
+    total = s_warp[31];
+    sync();
+    return before + incl - v;
+  };
+  // running maximum of the offsets: whatever they hold, the rows of all
+  // sequences are disjoint and inside q, so the tiles fit the workspace
+  int before_all = 0;
+  for (int base = 0; base <= p.B; base += THREADS) {
+    const int b = base + tid;
+    int v = b <= p.B ? min(max(p.q_offsets[b], 0), p.T) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, v, o);
+      if (lane >= o) v = max(v, up);
+    }
+    if (THREADS > 32) {
+      if (lane == 31) s_warp[warp] = v;
+      sync();
+      // lane w: what warp w reached
+      int all = static_cast<int>(s_warp[lane]), mine = lane < warp ? all : 0;
+      mine = __reduce_max_sync(0xFFFFFFFFu, mine);
+      all = __reduce_max_sync(0xFFFFFFFFu, all);
+      v = max(max(v, mine), before_all);
+      before_all = max(before_all, all);
+    } else {
+      v = max(v, before_all);
+      before_all = __shfl_sync(0xFFFFFFFFu, v, 31);
+    }
+    if (b <= p.B) p.starts[b] = v;
+    sync();
+  }
+  long long tiles = 0;
+  for (int base = 0; base < p.B; base += THREADS) {
+    const int b = base + tid;
+    long long n = 0, total;
+    if (b < p.B) n = (static_cast<long long>(load_seq(p, b).n) * p.G + ROWS - 1) / ROWS;
+    const long long at = scan(n, total);
+    if (b < p.B) p.tile_base[b] = static_cast<int>(tiles + at);
+    tiles += total;
+  }
+  if (tid == 0) p.tile_base[p.B] = static_cast<int>(tiles);
+  sync();
+  long long units = 0;
+  for (long long base = 0; base < tiles; base += THREADS) {
+    const long long f = base + tid;
+    long long n = 0, total;
+    if (f < tiles) {
+      int lo = 0, hi = p.B;  // largest b with tile_base[b] <= f
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.tile_base[mid] <= f) lo = mid;
+        else hi = mid;
+      }
+      const Seq s = load_seq(p, lo);
+      int u0, u1;
+      tile_units<ROWS>(p, s, static_cast<int>(f - p.tile_base[lo]), unit, u0, u1);
+      n = u1 - u0;
+    }
+    const long long at = scan(n, total);
+    if (f < tiles) p.unit_sum[f] = units + at;
+    units += total;
+  }
+  if (tid == 0) p.unit_sum[tiles] = units;
+}
+
 DEVINL long long total_units(const AttnParams& p) { return p.unit_sum[p.tile_base[p.B]] * p.Hkv; }
 DEVINL long long range_of(const AttnParams& p, long long total) {
   const long long r = (total + p.blocks - 1) / p.blocks;
@@ -451,7 +551,9 @@ DEVINL long long range_of(const AttnParams& p, long long total) {
 
 // Main kernel over 256-row tiles and 128-key units (kv4_prefill.cu).
 int attention_tiles(const AttnParams& p, int D, cudaStream_t s);
-// Main kernel over 16-row tiles and 128-key units, heads of 128 (kv4_decode.cu).
+// Main kernel over 16-row tiles and 128-key units, heads of 128 (kv4_decode.cu);
+// a warp of each block makes the schedule for up to kPlanHere sequences and tiles.
+constexpr int kPlanHere = 31;
 int attention_decode(const AttnParams& p, cudaStream_t s);
 
 }  // namespace kv4
