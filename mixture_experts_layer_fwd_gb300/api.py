@@ -716,7 +716,12 @@ def _kv_pools(pool: Optional[torch.Tensor], num_pages: int, device):
     """(pointer, layers, bytes between layers, bytes of a page) of uint8 [layers, num_pages, ...] or None."""
     if pool is None:
         return None, 0, 0, 16
-    _dev(pool, "pool", dtype=torch.uint8, device=device)
+    try:
+        ok = pool.dtype is _U8 and pool.device == device and pool.is_contiguous()
+    except AttributeError:
+        ok = False
+    if not ok:
+        _dev(pool, "pool", dtype=torch.uint8, device=device)
     if pool.dim() < 3 or pool.shape[1] != num_pages:
         raise ValueError(f"pool: expected [layers, {num_pages}, ...], got {tuple(pool.shape)}")
     layers = pool.shape[0]
@@ -725,6 +730,11 @@ def _kv_pools(pool: Optional[torch.Tensor], num_pages: int, device):
 
 
 def _index(t: torch.Tensor, name: str, device) -> int:
+    try:
+        if t.dtype is _I32 and t.dim() == 1 and t.device == device and t.is_contiguous():
+            return t.numel()
+    except AttributeError:
+        pass
     _dev(t, name, dtype=torch.int32, device=device)
     if t.dim() != 1:
         raise ValueError(f"{name}: expected one dimension")
