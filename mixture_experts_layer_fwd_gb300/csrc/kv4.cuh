@@ -22,5 +22,25 @@ __host__ __device__ constexpr int record_bytes(int P, int D) { return 2 * (codes
 inline bool page_size_ok(int P) { return P == 32 || P == 64 || P == 128; }
 inline bool head_dim_ok(int D) { return D == 64 || D == 128; }
 
+// Programmatic dependent launch: the next kernel of the call may start its
+// prologue now; and: wait for the results of the one before.
+DEVINL void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <class... Params, class... Args>
+inline int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
+  cudaLaunchAttribute a{};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &a, cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  if (e != cudaSuccess) {
+    set_cuda_error(e);
+    return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
 }  // namespace kv4
 }  // namespace moe

@@ -424,26 +424,6 @@ DEVINL void walk_range(const AttnParams& p, int unit, int block, long long x0, l
   use(end);
 }
 
-// Programmatic dependent launch: the next kernel of the call may start its
-// prologue now; and: wait for the results of the one before.
-DEVINL void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-DEVINL void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-template <class... Params, class... Args>
-inline int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s, Args... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid, cfg.blockDim = dim3(threads), cfg.dynamicSmemBytes = smem, cfg.stream = s;
-  cudaLaunchAttribute a{};
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &a, cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
-  if (e != cudaSuccess) {
-    set_cuda_error(e);
-    return MOE_ERR_CUDA;
-  }
-  return MOE_OK;
-}
-
 // The schedule (starts, tile_base, unit_sum) by a warp or a block of 1024
 // threads, which shares the 32 words s_warp.
 template <int ROWS, int THREADS>

@@ -168,6 +168,7 @@ DEVINL void copy_pages(const Pool& pool, const int* src, const int* dst, int n, 
 __global__ void __launch_bounds__(kPlan) extend_plan_kernel(State s, const int32_t* q_offsets, int T, Plan w,
                                                             unsigned int* err) {
   __shared__ int s_warp[32];
+  kv4::launch_dependents();
   if (blockIdx.x > 0) return carry_over(s);
   int need = 0;
   for (int base = 0; base < s.S; base += kPlan) {
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kPlan) extend_plan_kernel(State s, const int32
 
 __global__ void extend_apply_kernel(State s, const int32_t* q_offsets, int T, Plan w, long long* slots, int32_t* pos,
                                     unsigned int* err) {
+  kv4::wait_for_previous();
   const int r = blockIdx.x;
   if (r == s.S) {  // tokens of no row
     for (int t = max(0, q_offsets[s.S]) + threadIdx.x; t < T; t += blockDim.x) {
@@ -235,6 +237,7 @@ __global__ void extend_apply_kernel(State s, const int32_t* q_offsets, int T, Pl
 __global__ void __launch_bounds__(kPlan) fork_plan_kernel(State s, const int32_t* src, const int32_t* dst, int n, Plan w,
                                                           unsigned int* err) {
   __shared__ int s_warp[32];
+  kv4::launch_dependents();
   if (blockIdx.x > 0) return carry_over(s);
   int need = 0;
   for (int base = 0; base < n; base += kPlan) {
@@ -267,6 +270,7 @@ __global__ void __launch_bounds__(kPlan) fork_plan_kernel(State s, const int32_t
 
 __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(State s, const int32_t* src, const int32_t* dst, int n,
                                                                   Plan w, Pool pool, unsigned int* err) {
+  kv4::wait_for_previous();
   if (blockIdx.x >= n) return copy_pages(pool, w.list_b, w.list_a, w.count[0], s.N, n, err);
   const int i = blockIdx.x;
   const int len = w.row_a[i];
@@ -295,10 +299,14 @@ __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(State s, const
 }
 
 // -------------------------------------------------------------------- free
-__global__ void __launch_bounds__(kPlan) carry_kernel(State s) { carry_over(s); }
+__global__ void __launch_bounds__(kPlan) carry_kernel(State s) {
+  kv4::launch_dependents();
+  carry_over(s);
+}
 
 __global__ void free_apply_kernel(State s, const int32_t* rows, int n, unsigned int* err) {
   __shared__ int s_dup;
+  kv4::wait_for_previous();
   const int i = blockIdx.x, r = rows[i];
   if (r < 0 || r >= s.S) {
     if (threadIdx.x == 0) atomicOr(err, kErrBadIndex);
@@ -330,6 +338,7 @@ __global__ void free_apply_kernel(State s, const int32_t* rows, int n, unsigned 
 // fewest moves, and no page is both read and written.
 __global__ void __launch_bounds__(kPlan) compact_plan_kernel(State s, Plan w, int32_t* remap) {
   __shared__ int s_warp[32];
+  kv4::launch_dependents();
   if (blockIdx.x > 0) {
     const int id = (blockIdx.x - 1) * kPlan + threadIdx.x, step = (gridDim.x - 1) * kPlan;
     for (int p = id; p < s.N; p += step) {
@@ -368,6 +377,7 @@ __global__ void __launch_bounds__(kPlan) compact_plan_kernel(State s, Plan w, in
 
 __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(State s, Plan w, Pool pool, int32_t* remap,
                                                                      int small, unsigned int* err) {
+  kv4::wait_for_previous();
   const int moves = w.count[0], live = w.count[1];
   if (blockIdx.x >= small) return copy_pages(pool, w.list_b, w.list_a, moves, s.N, small, err);
   const long long id = static_cast<long long>(blockIdx.x) * kCopyThreads + threadIdx.x;
@@ -461,8 +471,7 @@ extern "C" int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* tab
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   extend_plan_kernel<<<1 + carry_blocks(s), kPlan, 0, st>>>(s, q_offsets, T, w, err);
   MOE_TRY(check_launch());
-  extend_apply_kernel<<<rows + 1, 128, 0, st>>>(s, q_offsets, T, w, slots, pos, err);
-  return check_launch();
+  return kv4::launch_after(extend_apply_kernel, dim3(rows + 1), 128, 0, st, s, q_offsets, T, w, slots, pos, err);
 }
 
 extern "C" int moe_kv_fork(const int32_t* src, const int32_t* dst, int n, const int32_t* table_in,
@@ -487,8 +496,7 @@ extern "C" int moe_kv_fork(const int32_t* src, const int32_t* dst, int n, const 
   fork_plan_kernel<<<1 + carry_blocks(s), kPlan, 0, st>>>(s, src, dst, n, w, err);
   MOE_TRY(check_launch());
   if (n == 0) return MOE_OK;
-  fork_apply_kernel<<<n + copy_blocks(p, n), kCopyThreads, 0, st>>>(s, src, dst, n, w, p, err);
-  return check_launch();
+  return kv4::launch_after(fork_apply_kernel, dim3(n + copy_blocks(p, n)), kCopyThreads, 0, st, s, src, dst, n, w, p, err);
 }
 
 extern "C" int moe_kv_free(const int32_t* rows_to_free, int n, const int32_t* table_in, const int32_t* lens_in,
@@ -508,8 +516,7 @@ extern "C" int moe_kv_free(const int32_t* rows_to_free, int n, const int32_t* ta
     MOE_TRY(check_launch());
   }
   if (n == 0) return MOE_OK;
-  free_apply_kernel<<<n, 128, 0, st>>>(s, rows_to_free, n, err);
-  return check_launch();
+  return kv4::launch_after(free_apply_kernel, dim3(n), 128, 0, st, s, rows_to_free, n, err);
 }
 
 extern "C" int moe_kv_compact(const int32_t* table_in, const int32_t* refs_in, int rows, int max_pages, int num_pages,
@@ -531,8 +538,8 @@ extern "C" int moe_kv_compact(const int32_t* table_in, const int32_t* refs_in, i
   const long long entries = std::max<long long>(static_cast<long long>(rows) * max_pages, num_pages / 2);
   const int small = static_cast<int>(
       std::max<long long>(1, std::min<long long>(num_sms(), (entries + 4 * kCopyThreads - 1) / (4 * kCopyThreads))));
-  compact_apply_kernel<<<small + copy_blocks(p, num_pages / 2), kCopyThreads, 0, st>>>(s, w, p, remap, small, err);
-  return check_launch();
+  return kv4::launch_after(compact_apply_kernel, dim3(small + copy_blocks(p, num_pages / 2)), kCopyThreads, 0, st, s, w, p,
+                           remap, small, err);
 }
 
 extern "C" int moe_kv_copy_pages(uint8_t* pool, int layers, long long layer_stride, long long page_bytes, int num_pages,
