@@ -24,7 +24,7 @@
 // Numbers are as in the 16-row kernel: codes times block scales and Q times a
 // power of two are exact in fp16, P is rounded to fp16, sums are fp32.
 //
-// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.98 ms, 1.41 PFLOP/s; the
+// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.99 ms, 1.39 PFLOP/s; the
 // same with heads of 64 0.88 ms.  What bounds it is the chain scores, softmax,
 // weights, next scores of a tile, since scores and weights share columns.  Half
 // a row per thread 1.17 against 1.21 ms, one tester of a barrier for the eight
