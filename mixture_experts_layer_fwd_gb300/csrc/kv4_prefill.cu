@@ -24,7 +24,7 @@
 // Numbers are as in the 16-row kernel: codes times block scales and Q times a
 // power of two are exact in fp16, P is rounded to fp16, sums are fp32.
 //
-// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.99 ms, 1.39 PFLOP/s; the
+// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.97 ms, 1.42 PFLOP/s; the
 // same with heads of 64 0.88 ms.  What bounds it is the chain scores, softmax,
 // weights, next scores of a tile, since scores and weights share columns.  Half
 // a row per thread 1.17 against 1.21 ms, one tester of a barrier for the eight
@@ -65,16 +65,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 3328, "between the operand tiles and the ring");
 
-// D[tmem] (+)= A[smem] * B[smem]^T from a whole converged warp.
-DEVINL void umma_f16_ss_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   // no memory clobber: loads of record bytes may move past stores to operand tiles
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
@@ -487,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           // cores idle while both are in their softmax.
           if (g == 1 || j > 0) wait_warp(&bars.turn[g], (j - (g == 0)) & 1, polls, p.err, abort);
           // O += P V, then S = Q K^T, which P lies over.  A rolled loop keeps what
-          // S needs out of the way of P's product: 0.98 against 1.05 ms unrolled.
+          // S needs out of the way of P's product: 0.98 against 1.05 ms unrolled.  One
+          // election for all of a product's instructions: 0.95 against 0.98.
 #pragma unroll 1
           for (int step = 0; step < 2; ++step) {
             if (step == 0) {
@@ -496,13 +487,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
                 pp ^= 1;
                 tc_fence_after();
                 const uint64_t b = dv + so * (C::K_BYTES >> 4);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < kKeys / 16; ++kk)
-                  umma_f16_ts_warp(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4),
-                                   idesc_f16_f32(128, D) | kMajorB, cur_first && kk == 0 ? 0u : 1u);
-                umma_commit_warp(&bars.ofull[g]);
-                umma_commit_warp(&bars.turn[g ^ 1]);
-                umma_commit_warp(&bars.vempty[so]);
+                  for (int kk = 0; kk < kKeys / 16; ++kk)
+                    umma_f16_ts(to, ts + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * (16 * 128 >> 4),
+                                idesc_f16_f32(128, D) | kMajorB, cur_first && kk == 0 ? 0u : 1u);
+                  umma_commit(&bars.ofull[g]);
+                  umma_commit(&bars.turn[g ^ 1]);
+                  umma_commit(&bars.vempty[so]);
+                }
               } else if (cur && lane == 0) {
                 mbar_arrive(&bars.vempty[so]);
               }
@@ -513,13 +506,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               }
               tc_fence_after();
               const uint64_t b = dk + st * (C::K_BYTES >> 4);
+              if (elect_one()) {
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
-                umma_f16_ss_warp(ts, dq + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t o = (kk >> 2) * (C::SUB_Q >> 4) + (kk & 3) * 2;
+                  umma_f16(ts, dq + o, b + o, idesc_f16_f32(128, kKeys), kk ? 1u : 0u);
+                }
+                umma_commit(&bars.sfull[g]);
+                umma_commit(&bars.kempty[st]);
               }
-              umma_commit_warp(&bars.sfull[g]);
-              umma_commit_warp(&bars.kempty[st]);
             } else if (more && lane == 0) {
               mbar_arrive(&bars.kempty[st]);
             }
