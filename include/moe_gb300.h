@@ -107,7 +107,8 @@ const char* moe_status_string(int status);
  * (thread-unsafe, diagnostic only). */
 const char* moe_last_cuda_error(void);
 
-/* Time limit of every device-side wait, in nanoseconds (default 1e9).
+/* Time limit of every device-side wait, in nanoseconds (default 1e9; the
+ * attention kernels count tests that take about as long).
  * ns == 0 restores the default. */
 int moe_set_wait_timeout_ns(unsigned long long ns);
 

@@ -264,9 +264,9 @@ DEVINL void item_keys(const AttnParams& p, const Item& t, int idx, int& lo, int&
 template <bool LAZY = false>
 DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned int* err, volatile int* abort) {
 #pragma unroll 1
-  for (uint32_t k = 0; !mbar_try_wait(bar, parity); ++k) {
+  for (uint32_t k = 0; !mbar_try_wait(bar, parity); k += LAZY ? 8 : 1) {
     if (LAZY) __nanosleep(200);
-    if (k == polls) {
+    if (k >= polls) {
       atomicOr(err, kErrTimeout);
       *abort = 1;
     }
@@ -274,9 +274,9 @@ DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned i
   }
   __syncwarp();
 }
-// Tests in a wait, each some tens of nanoseconds long.
+// Tests in a wait, each some tens of nanoseconds long (a LAZY one counts as eight).
 DEVINL uint32_t polls_of(unsigned long long timeout_ns) {
-  return static_cast<uint32_t>(min(timeout_ns / 32, 0xFFFFFFFFull));
+  return static_cast<uint32_t>(min(timeout_ns / 32, 0xFFFFFF00ull));
 }
 // One reader's (a warp's) place in an ItemRing.
 struct ItemReader {
