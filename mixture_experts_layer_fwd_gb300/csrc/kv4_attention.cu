@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
             [&](int k) { return k & 1 ? hb : 0; }, abort);
         it += t.n;
       }
-      return *static_cast<volatile int*>(abort) == 0;
+      return !given_up(abort);
     });
     if (*static_cast<volatile int*>(abort)) slot.drain(p);
     return;

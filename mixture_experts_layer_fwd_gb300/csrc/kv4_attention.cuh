@@ -278,6 +278,10 @@ DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned i
 DEVINL uint32_t polls_of(unsigned long long timeout_ns) {
   return static_cast<uint32_t>(min(timeout_ns / 32, 0xFFFFFF00ull));
 }
+// Whether the block has given up waiting: one answer for the whole warp, which
+// reads it after what it waited for.  (Lanes that decided each by itself could
+// part, and meet the next vote or warp-wide instruction apart.)
+DEVINL bool given_up(volatile int* abort) { return __any_sync(0xFFFFFFFFu, *abort != 0); }
 // One reader's (a warp's) place in an ItemRing.
 struct ItemReader {
   int i = 0;
@@ -285,7 +289,7 @@ struct ItemReader {
     const int k = i & (kItems - 1);
     wait_warp(&r.full[k], (i / kItems) & 1, polls, err, abort);
     Item t = r.item[k];
-    if (*abort) t.n = 0;
+    if (given_up(abort)) t.n = 0;
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[k]);
     ++i;
@@ -298,6 +302,7 @@ struct ItemWriter {
   DEVINL void put(ItemRing& r, const Item& t, uint32_t polls, unsigned int* err, volatile int* abort) {
     const int k = i & (kItems - 1);
     if (i >= kItems) wait_warp<true>(&r.empty[k], (i / kItems - 1) & 1, polls, err, abort);
+    if (given_up(abort)) return;  // some reader may not have read what lies there: all read the same items
     if ((threadIdx.x & 31) == 0) {
       r.item[k] = t;
       mbar_arrive(&r.full[k]);
@@ -340,7 +345,7 @@ struct Slot {
     int id = -2;  // page of copy k: -2 not looked up, -1 none
     uint64_t t0 = 0;
     while (__any_sync(0xFFFFFFFFu, k < all)) {
-      bool moved = false;
+      bool ready = false;
       if (k < all) {
         if (id == -2) {
           const int pg = page_of(k);
@@ -353,20 +358,23 @@ struct Slot {
             }
           }
         }
-        if (uses == 0 || mbar_test_wait(empty, (uses - 1) & 1)) {
-          if (id < 0) {
-            mbar_arrive(full);  // no key of this page
-          } else {
-            mbar_arrive_expect_tx(full, bytes);
-            bulk_load(to, pool + id * stride + offset_of(k), bytes, full);
-          }
-          ++uses;
-          k += slots;
-          id = -2;
-          moved = true;
-        }
+        ready = uses == 0 || mbar_test_wait(empty, (uses - 1) & 1);
       }
-      if (__any_sync(0xFFFFFFFFu, moved)) {
+      // (seen after the slot came back: a consumer that has given up hands its
+      // slots back unread, some of them with copies on the way)
+      if (given_up(abort)) return;
+      if (ready) {
+        if (id < 0) {
+          mbar_arrive(full);  // no key of this page
+        } else {
+          mbar_arrive_expect_tx(full, bytes);
+          bulk_load(to, pool + id * stride + offset_of(k), bytes, full);
+        }
+        ++uses;
+        k += slots;
+        id = -2;
+      }
+      if (__any_sync(0xFFFFFFFFu, ready)) {
         t0 = 0;
       } else {
         const uint64_t now = globaltimer_ns();
@@ -375,7 +383,6 @@ struct Slot {
           atomicOr(p.err, kErrTimeout);
           *abort = 1;
         }
-        if (*abort) return;
         __nanosleep(100);
       }
     }

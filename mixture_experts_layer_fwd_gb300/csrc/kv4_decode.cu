@@ -584,14 +584,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
             [&](int k) { return k < pages * it.n ? it.u * pages + k : p.max_pages; },  // a ghost: no bytes
             [&](int) { return v ? half : 0; },
             abort);
-        if (*static_cast<volatile int*>(abort)) break;
+        if (given_up(abort)) break;
       }
       if (*static_cast<volatile int*>(abort)) slot.drain(p);
     } else if (warp == kWalk) {
       ItemWriter out;
       walk_range<kRows>(sched, kKeys, blockIdx.x, x0, x1, range, [&](const Item& t) {
         out.put(bars.items, t, polls, p.err, abort);
-        return *static_cast<volatile int*>(abort) == 0;
+        return !given_up(abort);
       });
     } else {
       // ================================================================ products

@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           slot.feed(
               p, it, pages * it.n, half, 2 * half, [&](int k) { return it.u * pages + k; },
               [&](int) { return v ? half : 0; }, abort);
-          if (*static_cast<volatile int*>(abort)) break;
+          if (given_up(abort)) break;
         }
         if (*static_cast<volatile int*>(abort)) slot.drain(p);
       } else if (warp == kWalk) {
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
         ItemWriter out;
         walk_range<kRows>(p, kKeys, blockIdx.x, x0, x1, range, [&](const Item& t) {
           out.put(bars.items, t, polls, p.err, abort);
-          return *static_cast<volatile int*>(abort) == 0;
+          return !given_up(abort);
         });
       } else {
         // =================================================== matrix instructions
