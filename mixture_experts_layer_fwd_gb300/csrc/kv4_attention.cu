@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
       }
       return !given_up(abort);
     });
-    if (*static_cast<volatile int*>(abort)) slot.drain(p);
+    slot.land(p);
     return;
   }
 

@@ -274,6 +274,10 @@ DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned i
   }
   __syncwarp();
 }
+// For what the hardware has in hand when a block ends (copies, products): it
+// completes by itself, and has to before shared and tensor memory go to the next
+// block, so this is not the limit that callers set, which may be as short as they like.
+constexpr unsigned long long kLandNs = 1000000000ull;
 // Tests in a wait, each some tens of nanoseconds long (a LAZY one counts as eight).
 DEVINL uint32_t polls_of(unsigned long long timeout_ns) {
   return static_cast<uint32_t>(min(timeout_ns / 32, 0xFFFFFF00ull));
@@ -388,9 +392,10 @@ struct Slot {
     }
     if (to != nullptr) at = (at + all) % slots;
   }
-  // After a time-out elsewhere: stay until the copies in flight have landed.
-  DEVINL void drain(const AttnParams& p) {
-    if (uses > 0) mbar_wait_bounded(full, (uses - 1) & 1, p.timeout_ns, p.err, nullptr, true);
+  // Until the lane's last copy has landed: whoever gave up, no block ends with
+  // bytes on their way to its shared memory.
+  DEVINL void land(const AttnParams& p) {
+    if (uses > 0) mbar_wait_bounded(full, (uses - 1) & 1, kLandNs, p.err, nullptr, true);
   }
 };
 

@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
             abort);
         if (given_up(abort)) break;
       }
-      if (*static_cast<volatile int*>(abort)) slot.drain(p);
+      slot.land(p);
     } else if (warp == kWalk) {
       ItemWriter out;
       walk_range<kRows>(sched, kKeys, blockIdx.x, x0, x1, range, [&](const Item& t) {
@@ -638,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
         ++seq;
       }
       umma_commit_warp(&bars.end);
-      mbar_wait_warp(&bars.end, 0, 1000000000ull, p.err, nullptr);
+      mbar_wait_warp(&bars.end, 0, kLandNs, p.err, nullptr);
      }
     }
   }

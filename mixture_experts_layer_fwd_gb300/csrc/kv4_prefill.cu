@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               [&](int) { return v ? half : 0; }, abort);
           if (given_up(abort)) break;
         }
-        if (*static_cast<volatile int*>(abort)) slot.drain(p);
+        slot.land(p);
       } else if (warp == kWalk) {
         // ================================================================ walk
         ItemWriter out;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           }
         }
         umma_commit_warp(&bars.done);
-        mbar_wait_warp(&bars.done, 0, 1000000000ull, p.err, nullptr);
+        mbar_wait_warp(&bars.done, 0, kLandNs, p.err, nullptr);
        }
       }
     }
