@@ -108,7 +108,8 @@ const char* moe_status_string(int status);
 const char* moe_last_cuda_error(void);
 
 /* Time limit of every device-side wait, in nanoseconds (default 1e9; the
- * attention kernels count tests that take about as long).
+ * attention kernels count tests of 4000 ns each).  A block that gives up still
+ * waits for its own copies and products in flight (1e9 ns at most).
  * ns == 0 restores the default. */
 int moe_set_wait_timeout_ns(unsigned long long ns);
 
@@ -126,6 +127,10 @@ int moe_sync_status(void* stream);
  * error word and the kernel returns; the context stays usable.  Read the
  * result with moe_sync_status(). */
 int moe_selftest_wait_timeout(unsigned long long timeout_ns, void* stream);
+
+/* The same for the attention kernels' waits, which count tests; `lazy`: those
+ * that sleep between tests. */
+int moe_selftest_attention_wait_timeout(unsigned long long timeout_ns, int lazy, void* stream);
 
 /* ------------------------------------------------------------------- route
  * Router softmax and top-k with renormalised weights.

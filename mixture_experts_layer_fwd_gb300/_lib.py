@@ -55,6 +55,7 @@ SIGNATURES = {
     "moe_set_wait_timeout_ns": (c_int, [c_ull]),
     "moe_sync_status": (c_int, [c_void_p]),
     "moe_selftest_wait_timeout": (c_int, [c_ull, c_void_p]),
+    "moe_selftest_attention_wait_timeout": (c_int, [c_ull, c_int, c_void_p]),
     "moe_route": (c_int, [c_void_p, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
     "moe_route_ex": (c_int, [c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p]),
     "moe_permute_workspace_size": (c_size_t, [c_int, c_int, c_int]),

@@ -75,6 +75,11 @@ def moe_selftest_wait_timeout(timeout_ns: int, stream=None) -> None:
     check(load().moe_selftest_wait_timeout(int(timeout_ns), _stream(stream)), "moe_selftest_wait_timeout")
 
 
+def moe_selftest_attention_wait_timeout(timeout_ns: int, lazy: bool = False, stream=None) -> None:
+    check(load().moe_selftest_attention_wait_timeout(int(timeout_ns), 1 if lazy else 0, _stream(stream)),
+          "moe_selftest_attention_wait_timeout")
+
+
 def moe_route(logits: torch.Tensor, k: int, idx: Optional[torch.Tensor] = None,
               w: Optional[torch.Tensor] = None, stream=None, renorm: bool = True):
     """logits fp32 [T, E] -> (idx int32 [T, k], w fp32 [T, k]); renorm=False
@@ -848,7 +853,7 @@ def moe_kv_copy_pages(pool: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, 
 
 __all__ = ["MOE_FMT_BF16", "MOE_FMT_NVFP4", "MOE_FMT_MXFP8", "MOE_FMT_MXFP4", "moe_quant_mx", "MOE_EPI_STORE_BF16", "MOE_EPI_SWIGLU_BF16",
            "MOE_EPI_SWIGLU_NVFP4", "moe_version", "moe_sync_status", "moe_set_wait_timeout_ns",
-           "moe_selftest_wait_timeout", "moe_selftest_grid_barrier_timeout", "moe_route", "moe_permute",
+           "moe_selftest_wait_timeout", "moe_selftest_attention_wait_timeout", "moe_selftest_grid_barrier_timeout", "moe_route", "moe_permute",
            "moe_route_permute", "moe_quant_nvfp4", "MOE_EPI_SWIGLU_MX",
            "moe_permute_noalloc", "moe_grouped_gemm", "moe_combine", "moe_shared_gate",
            "moe_forward_workspace_size", "moe_forward", "moe_forward_profiled", "moe_forward_host",

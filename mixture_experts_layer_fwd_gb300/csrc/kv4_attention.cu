@@ -594,6 +594,20 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
   return launch_after(attn_rows16_kernel, dim3(p.blocks / kGroups), kThreads, smem, s, p, slots);
 }
 
+// A wait of the kernels above on a barrier that nothing arrives on.
+__global__ void attn_wait_selftest_kernel(unsigned int* err, unsigned long long timeout_ns, int lazy) {
+  __shared__ uint64_t bar;
+  __shared__ int abort;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar, 1);
+    abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (lazy) wait_warp<true>(&bar, 0, polls_of(timeout_ns), err, &abort);
+  else wait_warp(&bar, 0, polls_of(timeout_ns), err, &abort);
+}
+
 // Schedule, main kernel, joining.
 template <int ROWS, int D>
 int run(const AttnParams& p, int unit, cudaStream_t s) {
@@ -643,6 +657,13 @@ Layout layout(AttnParams& p, int D, void* ws) {
 
 }  // namespace
 
+int attention_wait_selftest(unsigned long long timeout_ns, int lazy, cudaStream_t s) {
+  unsigned int* err = device_error_word();
+  if (!err) return MOE_ERR_CUDA;
+  attn_wait_selftest_kernel<<<1, 32, 0, s>>>(err, timeout_ns, lazy);
+  return check_launch();
+}
+
 int attention(const AttnParams& p, int D, int rows, cudaStream_t s) {
   if (rows == kRows) return D == 128 ? run<kRows, 128>(p, kTileKeys, s) : run<kRows, 64>(p, p.P, s);
   return D == 128 ? run<kTileRows, 128>(p, kTileKeys, s) : run<kTileRows, 64>(p, kTileKeys, s);
@@ -652,6 +673,10 @@ int attention(const AttnParams& p, int D, int rows, cudaStream_t s) {
 }  // namespace moe
 
 using namespace moe;
+
+extern "C" int moe_selftest_attention_wait_timeout(unsigned long long timeout_ns, int lazy, void* stream) {
+  return kv4::attention_wait_selftest(timeout_ns, lazy, static_cast<cudaStream_t>(stream));
+}
 
 extern "C" size_t moe_kv4_attention_workspace_size(int T, int B, int Hq, int Hkv, int D) {
   if (T < 1 || B < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv || !kv4::head_dim_ok(D)) return 0;

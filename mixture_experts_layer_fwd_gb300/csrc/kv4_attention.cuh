@@ -255,16 +255,18 @@ DEVINL void item_keys(const AttnParams& p, const Item& t, int idx, int& lo, int&
   row_keys(p, s, idx / p.G, lo, hi);
 }
 
-// Bounded wait of a whole warp, every lane testing.  The test suspends the warp
-// in hardware for a few tens of cycles by itself (given a suspend time it
-// sleeps in steps that cost a round trip each).  The bound is a number of
-// tests: reading a clock in each of some thirty waits makes a third of the
-// program, which has to stay in the instruction cache.  LAZY: for warps that
-// nothing waits for soon.
+// Bounded wait of a whole warp, every lane testing.  A test that fails has
+// suspended the warp in hardware for kTestNs, unless the phase completed before
+// that (measured: 3.9 to 4.0 us, with a block's other warps idle, busy or
+// arriving on the same barrier; a suspend time given with the test changes
+// nothing).  So the bound is a number of tests: reading a clock in each of some
+// thirty waits makes a third of the program, which has to stay in the
+// instruction cache.  LAZY: for warps that nothing waits for soon.
+constexpr unsigned long long kTestNs = 4000;
 template <bool LAZY = false>
 DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned int* err, volatile int* abort) {
 #pragma unroll 1
-  for (uint32_t k = 0; !mbar_try_wait(bar, parity); k += LAZY ? 8 : 1) {
+  for (uint32_t k = 0; !mbar_try_wait(bar, parity); ++k) {
     if (LAZY) __nanosleep(200);
     if (k >= polls) {
       atomicOr(err, kErrTimeout);
@@ -278,9 +280,9 @@ DEVINL void wait_warp(uint64_t* bar, uint32_t parity, uint32_t polls, unsigned i
 // completes by itself, and has to before shared and tensor memory go to the next
 // block, so this is not the limit that callers set, which may be as short as they like.
 constexpr unsigned long long kLandNs = 1000000000ull;
-// Tests in a wait, each some tens of nanoseconds long (a LAZY one counts as eight).
+// Failing tests after which a wait gives up.
 DEVINL uint32_t polls_of(unsigned long long timeout_ns) {
-  return static_cast<uint32_t>(min(timeout_ns / 32, 0xFFFFFF00ull));
+  return static_cast<uint32_t>(min(timeout_ns / kTestNs, 0xFFFFFF00ull));
 }
 // Whether the block has given up waiting: one answer for the whole warp, which
 // reads it after what it waited for.  (Lanes that decided each by itself could
