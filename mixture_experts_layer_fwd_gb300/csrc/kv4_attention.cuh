@@ -402,7 +402,8 @@ struct Slot {
 };
 
 // Walks range `block` and hands its items to `use(item)`, the end mark (n == 0)
-// last; writes down what the range's two slots hold.  A whole warp calls it.
+// last; writes down what the range's two slots hold, also where `use` gives up
+// (false): the join that is queued behind goes by it.  A whole warp calls it.
 template <int ROWS, class Use>
 DEVINL void walk_range(const AttnParams& p, int unit, int block, long long x0, long long x1, long long range, Use use) {
   PartItem* notes = reinterpret_cast<PartItem*>(p.part_item) + 2 * block;
@@ -424,7 +425,7 @@ DEVINL void walk_range(const AttnParams& p, int unit, int block, long long x0, l
           notes[side] = q;
         }
       }
-      if (!use(t)) return;
+      if (!use(t)) break;  // given up: what was not noted is still marked below, the join reads it
       x += n;
       if (x >= x1) break;
       cursor_next<ROWS>(p, unit, c);

@@ -49,3 +49,46 @@ def test_attention_waits_give_up_near_their_limit(lazy, limit_us):
     t[1].record()
     assert m.moe_sync_status() == 5 and m.moe_sync_status() == 0
     assert limit_us / 2 <= 1000 * t[0].elapsed_time(t[1]) <= 2 * limit_us
+
+
+@pytest.mark.parametrize("limit_us", [0, 20, 60])
+@pytest.mark.parametrize("D,qs,kv", [
+    (64, [1] * 40, 8192),     # the 16-row kernel
+    (128, [1] * 15, 16384),   # the decode kernel that makes its own schedule
+    (128, [1] * 40, 8192),    # the one with a schedule in front
+    (64, [300, 90], 16384),   # the 256-row kernel
+    (128, [300, 90], 16384),
+])
+def test_attention_that_gives_up_stays_inside_its_buffers(D, qs, kv, limit_us):
+    """Whatever the workspace held before; the next call is right again.  Every
+    block has some 10 us of work and more copies than its ring takes: with no
+    time to wait it gives up, with more it may get through."""
+    m, Hkv, G, P = moe(), 2, 4, 64
+    T, B, Hq = sum(qs), len(qs), Hkv * G
+    gen = torch.Generator(DEV).manual_seed(21)
+    pool = torch.randint(0, 256, (64, Hkv, oa.record_bytes(P, D)), generator=gen, device=DEV, dtype=torch.uint8)
+    for first in (P * D // 2, P * D // 16 * 9 + P * D // 2):
+        pool[:, :, first:first + P * D // 16] = 0x38
+    g = torch.full((Hkv,), 0.01, device=DEV)
+    q = torch.randn(T, Hq, D, generator=gen, device=DEV).bfloat16()
+    args = (q, pool, g, g, dev(np.cumsum([0] + qs), I32), dev([kv - 5 * (i % 3) for i in range(B)], I32),
+            torch.randint(0, 64, (B, kv // P), generator=gen, device=DEV, dtype=I32))
+    want = m.moe_kv4_attention(*args)
+    assert torch.isfinite(want).all()
+    n, guard = want.numel(), 1 << 16
+    outs = torch.full((n + 2 * guard,), 3.0, dtype=torch.bfloat16, device=DEV)
+    lses = torch.full((T * Hq + 2 * guard,), 3.0, device=DEV)
+    size = m._lib.load().moe_kv4_attention_workspace_size(T, B, Hq, Hkv, D)
+    wss = torch.full((size + 2 * guard,), 0x7F, dtype=torch.uint8, device=DEV)
+    out, lse, ws = (t[guard:t.numel() - guard] for t in (outs, lses, wss))
+    try:
+        m.moe_set_wait_timeout_ns(max(1, 1000 * limit_us))
+        m.moe_kv4_attention(*args, out=out.view(want.shape), lse=lse.view(T, Hq), ws=ws)
+    finally:
+        m.moe_set_wait_timeout_ns(0)
+    status = m.moe_sync_status()
+    assert status == 5 or (status == 0 and limit_us > 0)
+    for t, v in ((outs, 3.0), (lses, 3.0), (wss, 0x7F)):
+        assert (t[:guard] == v).all() and (t[t.numel() - guard:] == v).all()
+    assert torch.equal(m.moe_kv4_attention(*args, ws=ws), want)
+    assert m.moe_sync_status() == 0
