@@ -32,7 +32,11 @@ class KV4Cache:
         self.table = torch.full((rows, max_pages), -1, dtype=torch.int32, device=dev)
         self.lens = torch.zeros(rows, dtype=torch.int32, device=dev)
         self.refs = torch.zeros(num_pages, dtype=torch.int32, device=dev)
+        # of the step that extend() made room for; None from the call on that moves
+        # rows or pages, since its slots may be another row's after that
         self.q_offsets: Optional[torch.Tensor] = None
+        self.slots: Optional[torch.Tensor] = None
+        self.pos: Optional[torch.Tensor] = None
 
     def _rows(self, rows: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
@@ -51,9 +55,10 @@ class KV4Cache:
                interleaved: bool = False, window: int = 0, scale: Optional[float] = None) -> torch.Tensor:
         """The step's tokens through a layer's attention: norms and rotation of q
         and k, k and v into the cache, attention of the rotated queries.  q bf16
-        [T, Hq, D], k and v bf16 [T, Hkv, D] in the order of extend()'s counts."""
+        [T, Hq, D], k and v bf16 [T, Hkv, D] in the order of extend()'s counts.
+        All layers of a step come before the next fork(), free() or compact()."""
         if self.q_offsets is None:
-            raise ValueError("extend() comes before attend()")
+            raise ValueError("extend() comes before attend(), and fork(), free() and compact() end its step")
         pool, g_k, g_v = self.pool[layer], self.g_k[layer], self.g_v[layer]
         q, _ = api.moe_qk_norm_rope(q, k, cos_sin, self.pos, wq=wq, wk=wk, eps=eps, interleaved=interleaved, v=v,
                                     pool=pool, g_k=g_k, g_v=g_v, slots=self.slots)
@@ -61,12 +66,16 @@ class KV4Cache:
 
     def fork(self, src: Sequence[int], dst: Sequence[int]) -> None:
         """Empty rows dst continue as forks of rows src."""
+        self.q_offsets = self.slots = self.pos = None
         api.moe_kv_fork(self._rows(src), self._rows(dst), self.table, self.lens, self.refs, self.pool, self.page_size,
                         inplace=True)
 
     def free(self, rows: Sequence[int]) -> None:
+        """Rows become empty."""
+        self.q_offsets = self.slots = self.pos = None
         api.moe_kv_free(self._rows(rows), self.table, self.lens, self.refs, self.page_size, inplace=True)
 
     def compact(self) -> torch.Tensor:
         """Moves the pages in use to the lowest ids; returns the new id of each page (-1: free)."""
+        self.q_offsets = self.slots = self.pos = None
         return api.moe_kv_compact(self.table, self.refs, self.pool, inplace=True)["remap"]

@@ -92,3 +92,23 @@ def test_attention_that_gives_up_stays_inside_its_buffers(D, qs, kv, limit_us):
         assert (t[:guard] == v).all() and (t[t.numel() - guard:] == v).all()
     assert torch.equal(m.moe_kv4_attention(*args, ws=ws), want)
     assert m.moe_sync_status() == 0
+
+
+# ------------------------------------------------------------------- the class
+@pytest.mark.parametrize("what", ["fork", "free", "compact"])
+def test_a_step_is_over_once_rows_or_pages_have_moved(what):
+    """Its slots may be another row's by then: nothing is written until the next extend."""
+    q, k, v, cs = inputs(40)
+    c = cache()
+    run(c, 0, 5, q, k, v, cs, [40])
+    run(c, 1, 5, q, k, v, cs, [33])
+    c.extend([1, 0, 0, 0, 0])
+    {"fork": lambda: c.fork([0], [2]), "free": lambda: c.free([1]), "compact": c.compact}[what]()
+    keep = c.pool.clone()
+    with pytest.raises(ValueError, match="extend"):
+        c.attend(0, q[:1], k[:1], v[:1], cs)
+    assert torch.equal(c.pool, keep)
+    c.extend([1, 0, 0, 0, 0])
+    for layer in range(LAYERS):
+        c.attend(layer, q[:1], k[:1], v[:1], cs)
+    assert moe().moe_sync_status() == 0
