@@ -43,6 +43,8 @@ class KV4Cache:
 
     def extend(self, counts: List[int]) -> None:
         """Room for counts[row] new tokens in each row: sets slots, pos and q_offsets for this step."""
+        if len(counts) != self.lens.numel() or any(n < 0 for n in counts):
+            raise ValueError(f"counts: expected {self.lens.numel()} numbers of new tokens, one per row, got {list(counts)}")
         offsets = [0]
         for n in counts:
             offsets.append(offsets[-1] + int(n))

@@ -112,3 +112,11 @@ def test_a_step_is_over_once_rows_or_pages_have_moved(what):
     for layer in range(LAYERS):
         c.attend(layer, q[:1], k[:1], v[:1], cs)
     assert moe().moe_sync_status() == 0
+
+
+@pytest.mark.parametrize("counts", [[3, -1, 0, 0, 0], [1, 2], [0] * 6])
+def test_counts_are_one_per_row_and_not_negative(counts):
+    c = cache()
+    with pytest.raises(ValueError, match="counts"):
+        c.extend(counts)
+    assert c.lens.tolist() == [0] * 5 and int(c.refs.sum()) == 0
