@@ -37,20 +37,28 @@ class KV4Cache:
         self.q_offsets: Optional[torch.Tensor] = None
         self.slots: Optional[torch.Tensor] = None
         self.pos: Optional[torch.Tensor] = None
+        self.kv_lens: Optional[torch.Tensor] = None
 
     def _rows(self, rows: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
 
     def extend(self, counts: List[int]) -> None:
-        """Room for counts[row] new tokens in each row: sets slots, pos and q_offsets for this step."""
+        """Room for counts[row] new tokens in each row: sets slots, pos, q_offsets
+        and kv_lens for this step.  A row that finds no free page, or has no room
+        in its table row, keeps its length; moe_sync_status() reports it, and the
+        step's attention sees no keys for its tokens (zeros)."""
         if len(counts) != self.lens.numel() or any(n < 0 for n in counts):
             raise ValueError(f"counts: expected {self.lens.numel()} numbers of new tokens, one per row, got {list(counts)}")
         offsets = [0]
         for n in counts:
             offsets.append(offsets[-1] + int(n))
-        self.q_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
-        r = api.moe_kv_extend(self.q_offsets, offsets[-1], self.table, self.lens, self.refs, self.page_size, inplace=True)
-        self.slots, self.pos = r["slots"], r["pos"]
+        T = offsets[-1]
+        q_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
+        r = api.moe_kv_extend(q_offsets, T, self.table, self.lens, self.refs, self.page_size, inplace=True)
+        self.q_offsets, self.slots, self.pos, self.kv_lens = q_offsets, r["slots"], r["pos"], self.lens
+        if T > 0:  # a row's first new token has no slot: none of them has
+            first = self.slots.index_select(0, q_offsets[:-1].clamp(max=T - 1))
+            self.kv_lens = self.lens.masked_fill(first < 0, 0)
 
     def attend(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
                wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -64,20 +72,20 @@ class KV4Cache:
         pool, g_k, g_v = self.pool[layer], self.g_k[layer], self.g_v[layer]
         q, _ = api.moe_qk_norm_rope(q, k, cos_sin, self.pos, wq=wq, wk=wk, eps=eps, interleaved=interleaved, v=v,
                                     pool=pool, g_k=g_k, g_v=g_v, slots=self.slots)
-        return api.moe_kv4_attention(q, pool, g_k, g_v, self.q_offsets, self.lens, self.table, scale=scale, window=window)
+        return api.moe_kv4_attention(q, pool, g_k, g_v, self.q_offsets, self.kv_lens, self.table, scale=scale, window=window)
 
     def fork(self, src: Sequence[int], dst: Sequence[int]) -> None:
         """Empty rows dst continue as forks of rows src."""
-        self.q_offsets = self.slots = self.pos = None
+        self.q_offsets = self.slots = self.pos = self.kv_lens = None
         api.moe_kv_fork(self._rows(src), self._rows(dst), self.table, self.lens, self.refs, self.pool, self.page_size,
                         inplace=True)
 
     def free(self, rows: Sequence[int]) -> None:
         """Rows become empty."""
-        self.q_offsets = self.slots = self.pos = None
+        self.q_offsets = self.slots = self.pos = self.kv_lens = None
         api.moe_kv_free(self._rows(rows), self.table, self.lens, self.refs, self.page_size, inplace=True)
 
     def compact(self) -> torch.Tensor:
         """Moves the pages in use to the lowest ids; returns the new id of each page (-1: free)."""
-        self.q_offsets = self.slots = self.pos = None
+        self.q_offsets = self.slots = self.pos = self.kv_lens = None
         return api.moe_kv_compact(self.table, self.refs, self.pool, inplace=True)["remap"]

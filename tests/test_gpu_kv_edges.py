@@ -120,3 +120,29 @@ def test_counts_are_one_per_row_and_not_negative(counts):
     with pytest.raises(ValueError, match="counts"):
         c.extend(counts)
     assert c.lens.tolist() == [0] * 5 and int(c.refs.sum()) == 0
+
+
+def test_a_row_without_room_gets_no_answer():
+    """Its queries see nothing, as long as it has no place for their keys; the other rows' answers stay."""
+    m = moe()
+    q, k, v, cs = inputs(100)
+    a, b = cache(pages=3), cache(pages=40)
+    for c in (a, b):
+        run(c, 0, 5, q, k, v, cs, [30])
+        run(c, 1, 5, q, k, v, cs, [31])
+    counts = [1, 40, 0, 2, 0]  # one page is left: row 1 needs two, row 3 one that is handed out after them
+    ys = []
+    for c in (a, b):
+        c.extend(counts)
+        ys.append(c.attend(0, q[:43], k[:43], v[:43], cs))
+    assert m.moe_sync_status() == 6
+    assert a.lens.tolist() == [31, 31, 0, 0, 0] and b.lens.tolist() == [31, 71, 0, 2, 0]
+    assert torch.equal(ys[0][:1], ys[1][:1]) and (ys[0][1:] == 0).all() and (ys[1][1:] != 0).any()
+    a.free([1])
+    a.extend([1, 0, 0, 2, 0])
+    b.extend([1, 0, 0, 0, 0])
+    y = a.attend(0, q[:3], k[:3], v[:3], cs)
+    assert torch.equal(y[:1], b.attend(0, q[:1], k[:1], v[:1], cs)) and (y[1:] != 0).any()
+    assert m.moe_sync_status() == 0
+    a.extend([0] * 5)  # a step without tokens
+    assert a.attend(0, q[:0], k[:0], v[:0], cs).shape[0] == 0
