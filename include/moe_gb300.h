@@ -557,7 +557,9 @@ size_t moe_kv_pages_workspace_size(int num_pages, int rows);
 
 /* Room for new tokens: row r gets the tokens q_offsets[r] .. q_offsets[r+1]
  * (int32 [rows + 1]) behind its lens[r]; slots int64 [T] and pos int32 [T]
- * are what moe_qk_norm_rope takes.  A row that finds no free page or has no
+ * are what moe_qk_norm_rope takes.  Offsets are used as attention uses them:
+ * inside the tokens, never falling; a token that no row has gets slot -1 and
+ * position 0.  A row that finds no free page or has no
  * room in its table row stays as it is, its slots are -1, and the failure is
  * reported by moe_sync_status() (MOE_ERR_PAGES / MOE_ERR_INVALID_ARG). */
 int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* table_in, const int32_t* lens_in,

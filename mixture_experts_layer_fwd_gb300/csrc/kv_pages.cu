@@ -42,6 +42,7 @@ struct Plan {
   int* list_b;  // [N]
   int* row_a;   // [rows]
   int* row_b;   // [rows]
+  int* starts;  // [rows + 1] q_offsets as used
 };
 
 Plan carve(void* ws, int N, int rows, size_t* bytes) {
@@ -52,6 +53,7 @@ Plan carve(void* ws, int N, int rows, size_t* bytes) {
   p.list_b = c.take<int>(N);
   p.row_a = c.take<int>(rows);
   p.row_b = c.take<int>(rows);
+  p.starts = c.take<int>(rows + 1);
   if (bytes) *bytes = c.used;
   return p;
 }
@@ -166,17 +168,35 @@ DEVINL void copy_pages(const Pool& pool, const int* src, const int* dst, int n, 
 }
 
 // ------------------------------------------------------------------ extend
+// The offsets are read as attention reads them: inside the tokens, a running
+// maximum, so that whatever they hold each token has one row at most.
 __global__ void __launch_bounds__(kPlan) extend_plan_kernel(State s, const int32_t* q_offsets, int T, Plan w,
                                                             unsigned int* err) {
   __shared__ int s_warp[32];
   kv4::launch_dependents();
   if (blockIdx.x > 0) return carry_over(s);
-  int need = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int need = 0, reached = min(max(q_offsets[0], 0), T);  // largest offset so far
+  if (threadIdx.x == 0) w.starts[0] = reached;
   for (int base = 0; base < s.S; base += kPlan) {
     const int r = base + threadIdx.x;
+    int end = r < s.S ? min(max(q_offsets[r + 1], 0), T) : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, end, o);
+      if (lane >= o) end = max(end, up);
+    }
+    if (lane == 31) s_warp[warp] = end;
+    __syncthreads();
+    const int of_warp = s_warp[lane];
+    const int before = max(reached, __reduce_max_sync(0xFFFFFFFFu, lane < warp ? of_warp : 0));
+    const int up = __shfl_up_sync(0xFFFFFFFFu, end, 1);
+    const int n = max(before, end) - (lane > 0 ? max(before, up) : before);
+    reached = max(reached, __reduce_max_sync(0xFFFFFFFFu, of_warp));
+    __syncthreads();  // s_warp has been read
     int more = 0;
     if (r < s.S) {
-      const int n = max(0, min(q_offsets[r + 1], T) - max(q_offsets[r], 0));
+      w.starts[r + 1] = max(before, end);
       const int len = max(0, s.lens_in[r]);
       const long long want = (static_cast<long long>(len) + n + s.P - 1) / s.P;
       if (n > 0 && want > s.M) {
@@ -198,18 +218,19 @@ __global__ void __launch_bounds__(kPlan) extend_plan_kernel(State s, const int32
   if (threadIdx.x == 0) w.count[0] = found;
 }
 
-__global__ void extend_apply_kernel(State s, const int32_t* q_offsets, int T, Plan w, long long* slots, int32_t* pos,
-                                    unsigned int* err) {
+__global__ void extend_apply_kernel(State s, int T, Plan w, long long* slots, int32_t* pos, unsigned int* err) {
   kv4::wait_for_previous();
   const int r = blockIdx.x;
-  if (r == s.S) {  // tokens of no row
-    for (int t = max(0, q_offsets[s.S]) + threadIdx.x; t < T; t += blockDim.x) {
-      slots[t] = -1;
-      pos[t] = 0;
+  if (r == s.S) {  // tokens of no row: in front of the first one's and behind the last one's
+    const int first = w.starts[0], last = w.starts[s.S];
+    for (int t = threadIdx.x; t < first + T - last; t += blockDim.x) {
+      const int at = t < first ? t : last + t - first;
+      slots[at] = -1;
+      pos[at] = 0;
     }
     return;
   }
-  const int t0 = max(0, q_offsets[r]), t1 = min(T, q_offsets[r + 1]);
+  const int t0 = w.starts[r], t1 = w.starts[r + 1];
   const int rank = w.row_a[r], more = w.row_b[r];
   const int len = max(0, s.lens[r]);
   const bool ok = rank >= 0 && (more == 0 || rank + more <= w.count[0]);
@@ -472,7 +493,7 @@ extern "C" int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* tab
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   extend_plan_kernel<<<1 + carry_blocks(s), kPlan, 0, st>>>(s, q_offsets, T, w, err);
   MOE_TRY(check_launch());
-  return kv4::launch_after(extend_apply_kernel, dim3(rows + 1), 128, 0, st, s, q_offsets, T, w, slots, pos, err);
+  return kv4::launch_after(extend_apply_kernel, dim3(rows + 1), 128, 0, st, s, T, w, slots, pos, err);
 }
 
 extern "C" int moe_kv_fork(const int32_t* src, const int32_t* dst, int n, const int32_t* table_in,

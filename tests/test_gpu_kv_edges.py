@@ -146,3 +146,33 @@ def test_a_row_without_room_gets_no_answer():
     assert m.moe_sync_status() == 0
     a.extend([0] * 5)  # a step without tokens
     assert a.attend(0, q[:0], k[:0], v[:0], cs).shape[0] == 0
+
+
+# ---------------------------------------------------------------------- extend
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("rows,T,offsets", [
+    (3, 90, [7, 20, 20, 60]),           # tokens in front of the rows and behind them
+    (3, 90, [90, 90, 90, 90]),
+    (4, 90, [5, 40, 10, 70, 60]),       # offsets that fall
+    (4, 90, [-9, 30, 1 << 30, 3, -1]),  # and leave the tokens
+    (2500, 6000, None),                 # more rows than a block has threads
+])
+def test_extend_reads_its_offsets_as_attention_does(rows, T, offsets, inplace):
+    """Inside the tokens and never falling; a token that no row has goes nowhere."""
+    m, P = moe(), 32
+    rng = np.random.default_rng(rows)
+    if offsets is None:
+        offsets = np.sort(rng.integers(11, T - 7, rows + 1))
+        offsets[rng.integers(0, rows, 200)] -= 300
+    used = np.maximum.accumulate(np.clip(offsets, 0, T))
+    s = oa.Pages([[-1] * 9 for _ in range(rows)], [0] * rows, [0] * (rows + 400), P)
+    s.extend([3 * (r % 5) for r in range(rows)])
+    table, lens, refs = state(s)
+    slots, pos, failed = s.extend([int(n) for n in np.diff(used)])
+    assert not failed
+    before, after = int(used[0]), T - int(used[-1])
+    junk = dict(slots=torch.full((T,), 5, dtype=torch.int64, device=DEV), pos=torch.full((T,), 7, dtype=I32, device=DEV))
+    o = m.moe_kv_extend(dev(offsets, I32), T, table, lens, refs, P, inplace=inplace, out=junk)
+    same(o, s)
+    assert o["slots"].cpu().tolist() == [-1] * before + slots + [-1] * after
+    assert o["pos"].cpu().tolist() == [0] * before + pos + [0] * after
