@@ -552,7 +552,9 @@ int moe_kv4_attention(const uint16_t* q, long long q_stride, int T, int Hq,
 /* Operations on pages.  Each reads *_in and writes *_out, which may be the
  * same arrays (in place) or others (then everything is carried over).  Pages
  * are taken lowest free id first, so the result is a function of the state.
- * `rows` of the workspace: the table's rows, or n where that is larger. */
+ * `rows` of the workspace: the table's rows, or n where that is larger.
+ * With rows == 0, where table and lens may be NULL, refs is carried over and
+ * nothing else is read or written (no slots, no positions, no reports). */
 size_t moe_kv_pages_workspace_size(int num_pages, int rows);
 
 /* Room for new tokens: row r gets the tokens q_offsets[r] .. q_offsets[r+1]

@@ -774,6 +774,10 @@ def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: to
             r[name] = _empty((T,), dt, dev, stream)
         else:
             _dev(r[name], name, dtype=dt, shape=(T,), device=dev)
+    if S == 0:  # no row has the tokens
+        with torch.cuda.stream(stream):
+            r["slots"].fill_(-1)
+            r["pos"].zero_()
     lib = load()
     ws = _empty(lib.moe_kv_pages_workspace_size(N, S), torch.uint8, dev, stream)
     check(lib.moe_kv_extend(_ptr(q_offsets), T, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
@@ -793,6 +797,8 @@ def moe_kv_fork(src: torch.Tensor, dst: torch.Tensor, table: torch.Tensor, lens:
     n = _index(src, "src", dev)
     if _index(dst, "dst", dev) != n:
         raise ValueError("dst: expected as many rows as src")
+    if n > 0 and S == 0:
+        raise ValueError("src: the table has no rows")
     base, layers, layer_stride, page_bytes = _kv_pools(pool, N, dev)
     o = out or {}
     r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
@@ -811,6 +817,8 @@ def moe_kv_free(rows: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, ref
     """Rows (int32 [n]) become empty.  Returns dict(table, lens, refs)."""
     S, M, N = _kv_state(table, refs, lens)
     n = _index(rows, "rows", table.device)
+    if n > 0 and S == 0:
+        raise ValueError("rows: the table has no rows")
     o = out or {}
     r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
              lens=_like(o.get("lens"), "lens", lens, inplace, stream),

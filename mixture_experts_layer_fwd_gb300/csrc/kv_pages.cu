@@ -459,6 +459,13 @@ int carry_blocks(const State& s) {
   const long long n = std::max<long long>(static_cast<long long>(s.S) * s.M, s.N);
   return static_cast<int>(std::max<long long>(1, std::min<long long>(num_sms(), (n + 4 * kPlan - 1) / (4 * kPlan))));
 }
+// A table without rows: what there is to carry over.
+int carry_refs(const State& s, void* stream) {
+  if (s.refs == s.refs_in) return MOE_OK;
+  if (!s.refs || !s.refs_in) return MOE_ERR_INVALID_ARG;
+  carry_kernel<<<1 + carry_blocks(s), kPlan, 0, static_cast<cudaStream_t>(stream)>>>(s);
+  return check_launch();
+}
 int copy_blocks(const Pool& p, long long most) {
   const long long items = most * p.layers * ((p.page_bytes + kPart - 1) / kPart);
   return static_cast<int>(std::min<long long>(items, num_sms() * 8));
@@ -483,7 +490,7 @@ extern "C" int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* tab
   State s{table_in, lens_in, refs_in, table_out, lens_out, refs_out, rows, max_pages, num_pages, page_size};
   if (T < 0) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_state(s));
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return carry_refs(s, stream);
   if (!q_offsets || !lens_in || !lens_out || !aligned(q_offsets, 4)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!slots || !pos || !aligned(slots, 8) || !aligned(pos, 4))) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(ws, ws_bytes, num_pages, rows));
@@ -507,7 +514,7 @@ extern "C" int moe_kv_fork(const int32_t* src, const int32_t* dst, int n, const 
   if (n > 65536) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_state(s));
   MOE_TRY(check_pool(p));
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return carry_refs(s, stream);
   if (!lens_in || !lens_out || (n > 0 && (!src || !dst || !aligned(src, 4) || !aligned(dst, 4))))
     return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(ws, ws_bytes, num_pages, std::max(rows, n)));
@@ -528,7 +535,7 @@ extern "C" int moe_kv_free(const int32_t* rows_to_free, int n, const int32_t* ta
   if (n < 0) return MOE_ERR_INVALID_ARG;
   if (n > 65536) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(check_state(s));
-  if (rows == 0) return MOE_OK;
+  if (rows == 0) return carry_refs(s, stream);
   if (!lens_in || !lens_out || (n > 0 && (!rows_to_free || !aligned(rows_to_free, 4)))) return MOE_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();
   if (!err) return MOE_ERR_CUDA;

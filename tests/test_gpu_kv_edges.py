@@ -176,3 +176,24 @@ def test_extend_reads_its_offsets_as_attention_does(rows, T, offsets, inplace):
     same(o, s)
     assert o["slots"].cpu().tolist() == [-1] * before + slots + [-1] * after
     assert o["pos"].cpu().tolist() == [0] * before + pos + [0] * after
+
+
+# --------------------------------------------------------------------- no rows
+def test_page_operations_of_no_rows():
+    m = moe()
+    i = lambda *s: torch.zeros(*s, dtype=I32, device=DEV)  # noqa: E731
+    refs = dev([3, 0, 1, 0, 2, 0, 0, 0], I32)
+    junk = lambda: dict(refs=torch.full((8,), 77, dtype=I32, device=DEV))  # noqa: E731
+    slots, pos = torch.full((5,), 9, dtype=torch.int64, device=DEV), torch.full((5,), 9, dtype=I32, device=DEV)
+    o = m.moe_kv_extend(dev([2], I32), 5, i(0, 4), i(0), refs, 32, out=dict(junk(), slots=slots, pos=pos))
+    assert torch.equal(o["refs"], refs) and o["slots"].tolist() == [-1] * 5 and o["pos"].tolist() == [0] * 5
+    assert m.moe_kv_extend(dev([0], I32), 0, i(0, 4), i(0), refs, 32, out=junk())["refs"].equal(refs)
+    assert m.moe_kv_fork(i(0), i(0), i(0, 4), i(0), refs, out=junk())["refs"].equal(refs)
+    assert m.moe_kv_free(i(0), i(0, 4), i(0), refs, out=junk())["refs"].equal(refs)
+    with pytest.raises(ValueError, match="no rows"):
+        m.moe_kv_fork(i(1), i(1), i(0, 4), i(0), refs)
+    with pytest.raises(ValueError, match="no rows"):
+        m.moe_kv_free(i(1), i(0, 4), i(0), refs)
+    o = m.moe_kv_compact(i(0, 4), refs, out=junk())
+    assert o["refs"].tolist() == [3, 2, 1, 0, 0, 0, 0, 0] and o["remap"].tolist() == [0, -1, 2, -1, 1, -1, -1, -1]
+    assert m.moe_sync_status() == 0
