@@ -433,10 +433,11 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(Pool pool, const int
 int check_state(const State& s) {
   if (s.S < 0 || s.M < 1 || s.N < 1) return MOE_ERR_INVALID_ARG;
   if (!kv4::page_size_ok(s.P) || s.N > (1 << 27) || s.S > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  // (with no rows too: a compaction reads refs all the same, 16 bytes at a time)
+  if (!s.refs_in || !s.refs || !aligned(s.refs_in, 16) || !aligned(s.refs, 16)) return MOE_ERR_INVALID_ARG;
   if (s.S == 0) return MOE_OK;
-  if (!s.table_in || !s.table || !s.refs_in || !s.refs) return MOE_ERR_INVALID_ARG;
-  if (!aligned(s.table_in, 4) || !aligned(s.table, 4) || !aligned(s.lens_in, 4) || !aligned(s.lens, 4) ||
-      !aligned(s.refs_in, 16) || !aligned(s.refs, 16))
+  if (!s.table_in || !s.table) return MOE_ERR_INVALID_ARG;
+  if (!aligned(s.table_in, 4) || !aligned(s.table, 4) || !aligned(s.lens_in, 4) || !aligned(s.lens, 4))
     return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
@@ -462,7 +463,6 @@ int carry_blocks(const State& s) {
 // A table without rows: what there is to carry over.
 int carry_refs(const State& s, void* stream) {
   if (s.refs == s.refs_in) return MOE_OK;
-  if (!s.refs || !s.refs_in) return MOE_ERR_INVALID_ARG;
   carry_kernel<<<1 + carry_blocks(s), kPlan, 0, static_cast<cudaStream_t>(stream)>>>(s);
   return check_launch();
 }
@@ -555,7 +555,7 @@ extern "C" int moe_kv_compact(const int32_t* table_in, const int32_t* refs_in, i
   Pool p{pool, layers, layer_stride, page_bytes};
   MOE_TRY(check_state(s));
   MOE_TRY(check_pool(p));
-  if (!refs_in || !refs_out || !remap || !aligned(remap, 4)) return MOE_ERR_INVALID_ARG;
+  if (!remap || !aligned(remap, 4)) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(ws, ws_bytes, num_pages, 0));
   unsigned int* err = device_error_word();
   if (!err) return MOE_ERR_CUDA;

@@ -110,6 +110,13 @@ def test_page_operations_host_checks(lib, name):
     assert lib.moe_kv_copy_pages(P(4104), 1, 64, 16, 4, A, A, 2, None) == INVALID
 
 
+@pytest.mark.parametrize("name", ["extend", "fork", "free", "compact"])
+def test_page_operations_check_refs_of_a_table_without_rows(lib, name):
+    """They are read 16 bytes at a time with no rows too."""
+    assert pages_call(lib, name, S=0, refs=P(4100)) == INVALID
+    assert pages_call(lib, name, S=0, refs=None) == INVALID
+
+
 def test_status_of_missing_pages_has_a_name(lib):
     assert lib.moe_status_string(6) == b"MOE_ERR_PAGES"
 
