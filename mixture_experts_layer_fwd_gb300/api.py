@@ -504,6 +504,7 @@ def _raw_stream(stream, t: torch.Tensor) -> int:
 # what counts: each looks at its tensors with these predicates (half the cost of
 # the checks that name what is wrong) and falls back to those checks, which
 # raise, only where one of them says no.
+_INT_MAX = 2 ** 31 - 1  # a longer window is as good as none; ctypes would cut it off silently
 _BF16, _F32, _I32, _I64, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8
 
 
@@ -669,7 +670,7 @@ def moe_kv4_attention(q: torch.Tensor, pool: torch.Tensor, g_k: torch.Tensor, g_
     check(lib.moe_kv4_attention(
         q.data_ptr(), _token_stride(q), T, Hq, pool.data_ptr(), num_pages, page_bytes * 8 // (9 * D), Hkv, D,
         g_k.data_ptr(), g_v.data_ptr(), q_offsets.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), B, max_pages,
-        D ** -0.5 if scale is None else scale, 1 if causal else 0, window, out.data_ptr(),
+        D ** -0.5 if scale is None else scale, 1 if causal else 0, min(window, _INT_MAX), out.data_ptr(),
         None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream, q)),
         "moe_kv4_attention")
     return out

@@ -705,7 +705,10 @@ extern "C" int moe_kv4_attention(const uint16_t* q, long long q_stride, int T, i
   p.q = q, p.q_stride = q_stride, p.pool = pool, p.g_k = g_k, p.g_v = g_v;
   p.q_offsets = q_offsets, p.kv_lens = kv_lens, p.table = table, p.out = out, p.lse = lse;
   p.T = T, p.B = B, p.Hq = Hq, p.Hkv = Hkv, p.G = Hq / Hkv, p.num_pages = num_pages, p.P = page_size;
-  p.max_pages = max_pages, p.causal = causal, p.window = window, p.scale = scale;
+  p.max_pages = max_pages, p.causal = causal, p.scale = scale;
+  // a window as long as the table is none; a longer one could overflow with a
+  // query in front of the first key (2^24 of them at most)
+  p.window = static_cast<int>(std::min(static_cast<long long>(window), static_cast<long long>(max_pages) * page_size));
   p.timeout_ns = wait_timeout_ns();
   p.err = device_error_word();
   if (!p.err) return MOE_ERR_CUDA;

@@ -197,3 +197,15 @@ def test_page_operations_of_no_rows():
     o = m.moe_kv_compact(i(0, 4), refs, out=junk())
     assert o["refs"].tolist() == [3, 2, 1, 0, 0, 0, 0, 0] and o["remap"].tolist() == [0, -1, 2, -1, 1, -1, -1, -1]
     assert m.moe_sync_status() == 0
+
+
+# --------------------------------------------------------------------- windows
+@pytest.mark.parametrize("D,qs", [(64, [3, 1]), (128, [3, 1]), (64, [400, 1]), (128, [400, 1])])
+def test_a_window_that_never_ends_is_none(D, qs):
+    """Also where a sequence has more queries than keys and these fill several tiles."""
+    m = moe()
+    c = attn_case(D, 1, 16 if qs[0] < 100 else 1, 32, qs, [max(2, qs[0] - 90), 300], seed=22)
+    args = attn_args(c)
+    want = m.moe_kv4_attention(*args, scale=0.1)
+    for window in (2 ** 31 - 1, 2 ** 31 - 9, 2 ** 31, 2 ** 32 + 5, 1 << 30):
+        assert torch.equal(m.moe_kv4_attention(*args, scale=0.1, window=window), want)
