@@ -536,6 +536,8 @@ int moe_qk_norm_rope(const uint16_t* q, long long q_stride, const uint16_t* k, l
  * `causal` only t <= p, if window > 0 (causal only) only t > p - window.
  *   out[t][h] = sum_j softmax_j(scale * q . k_j) v_j;  0 where no key is seen
  *   lse[t][h] = log sum_j exp(scale * q . k_j) (fp32 [T][Hq] or NULL), -inf there
+ * A row of (t, h) one of whose scores is not a number is not a number either,
+ * lse included; the other rows are not touched by it.
  * Hq % Hkv == 0; query head h reads kv head h / (Hq / Hkv).  q bf16 [T][Hq][D]
  * with q_stride elements between tokens, out bf16 [T][Hq][D].  Rows of no
  * sequence are not written.  Offsets that fall, lengths past the table and

@@ -56,11 +56,11 @@ DEVINL void write_row(const AttnParams& p, const PartItem& t, int r, float m, fl
                       const float* o, int V) {
   const int idx = t.row0 + r, tok = idx / p.G;
   const long long row = static_cast<long long>(t.q0 + tok) * p.Hq + t.h * p.G + (idx - tok * p.G);
-  const float inv = l > 0.0f ? __ldg(p.g_v + t.h) / l : 0.0f;
+  const float inv = row_factor(__ldg(p.g_v + t.h), l);
   uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + row * D) + lane * (V / 2);
 #pragma unroll
   for (int v = 0; v < V / 2; ++v) dst[v] = pack_bf16x2(o[2 * v] * inv, o[2 * v + 1] * inv);
-  if (p.lse && lane == 0) p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+  if (p.lse && lane == 0) p.lse[row] = row_lse(m, l);
 }
 
 // Few rows.  With many parts (one context over the whole GPU has a hundred) a
@@ -557,11 +557,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
         if (whole) {
           const int idx = t.row0 + r, tok = idx / p.G;
           const long long row = static_cast<long long>(t.q0 + tok) * p.Hq + t.h * p.G + (idx - tok * p.G);
-          const float inv = ll > 0.0f ? __ldg(p.g_v + t.h) / ll : 0.0f;
+          const float inv = row_factor(__ldg(p.g_v + t.h), ll);
           *reinterpret_cast<uint2*>(p.out + row * D + col) =
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-          if (p.lse && q == 0 && part == 0)
-            p.lse[row] = ll > 0.0f ? (mm + log2f(ll) - kShift) * (1.0f / kLog2e) : -INFINITY;
+          if (p.lse && q == 0 && part == 0) p.lse[row] = row_lse(mm, ll);
         } else {
           *reinterpret_cast<float4*>(p.part_o + (slot * kRows + r) * D + col) = a;
           if (q == 0 && part == 0) {

@@ -84,6 +84,14 @@ DEVINL void row_scale(float scale_gk, uint32_t top, float& up, float& sc) {
   if (sc == 0.0f) sc = 1.0f, up = 0.0f;
 }
 
+// What a row's output is multiplied by, and its lse, from the sum and maximum of
+// its weights.  A sum of 0 is a row that sees no key; one that is not a number
+// (a query or a key is not) makes the row's answer none either.
+DEVINL float row_factor(float gv, float l) { return l == 0.0f ? 0.0f : gv / l; }
+DEVINL float row_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l) - kShift) * (1.0f / kLog2e);
+}
+
 struct AttnParams {
   const uint16_t* q;  // bf16 [T][Hq][D], q_stride elements between tokens
   long long q_stride;

@@ -435,10 +435,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
             p.part_ml[static_cast<long long>(it.slot) * 2 * kRows + r] = mm;
             p.part_ml[(static_cast<long long>(it.slot) * 2 + 1) * kRows + r] = sum;
           } else {
-            const float inv = sum > 0.0f ? gv / sum : 0.0f;
+            const float inv = row_factor(gv, sum);
             f[0] *= inv, f[1] *= inv;
-            if (p.lse && r < it.rows)
-              p.lse[bars.row[par][r]] = sum > 0.0f ? (mm + log2f(sum) - kShift) * (1.0f / kLog2e) : -INFINITY;
+            if (p.lse && r < it.rows) p.lse[bars.row[par][r]] = row_lse(mm, sum);
           }
           bars.fac[0][r] = f[0], bars.fac[1][r] = f[1];
         }

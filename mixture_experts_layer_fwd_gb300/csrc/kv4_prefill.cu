@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
           const int tok = idx / p.G;
           const long long row = static_cast<long long>(it.q0 + tok) * p.Hq + it.h * p.G + (idx - tok * p.G);
           const bool whole = it.slot < 0, have = rr < it.rows;
-          const float inv = l > 0.0f ? gv / l : 0.0f;
+          const float inv = row_factor(gv, l);
 #pragma unroll 1
           for (int q = 0; q < D / 64; ++q) {
             uint32_t o[32];
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
               p.part_ml[static_cast<long long>(it.slot) * 2 * kRows + rr] = m;
               p.part_ml[(static_cast<long long>(it.slot) * 2 + 1) * kRows + rr] = l;
             } else if (p.lse && have) {
-              p.lse[row] = l > 0.0f ? (m + log2f(l) - kShift) * (1.0f / kLog2e) : -INFINITY;
+              p.lse[row] = row_lse(m, l);
             }
           }
           tc_fence_before();

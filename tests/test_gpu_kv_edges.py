@@ -209,3 +209,44 @@ def test_a_window_that_never_ends_is_none(D, qs):
     want = m.moe_kv4_attention(*args, scale=0.1)
     for window in (2 ** 31 - 1, 2 ** 31 - 9, 2 ** 31, 2 ** 32 + 5, 1 << 30):
         assert torch.equal(m.moe_kv4_attention(*args, scale=0.1, window=window), want)
+
+
+# -------------------------------------------------------------------------- NaN
+def check_poisoned(c, clean, out, lse, poisoned, P, scale):
+    """Rows (token, head) in `poisoned` are NaN throughout, the others within the bound of tests/test_gpu_kv4.py."""
+    ref, rlse, weight, all_v = oa.attention(to_np_f32(clean["q"]), clean["pool"], c["gk"], c["gv"], c["starts"], c["lens"],
+                                            c["table"], scale, P, True, 0)
+    got, gl = to_np_f32(out).astype(np.float64), lse.cpu().numpy()
+    assert np.isnan(got[poisoned]).all() and np.isnan(gl[poisoned]).all()
+    bad = np.abs(got - ref) > 2.0 ** -8 * np.abs(ref) + 2.0 ** -10 * weight + 2.0 ** -32 * all_v
+    assert not bad[~poisoned].any() and not np.isnan(got[~poisoned]).any()
+    assert np.abs(gl[~poisoned] - rlse[~poisoned]).max(initial=0) <= 5e-4
+
+
+@pytest.mark.parametrize("kv", [100, 3000])  # one block's, and many blocks'
+@pytest.mark.parametrize("D,qs", KERNELS)
+def test_a_query_that_is_not_a_number_answers_with_none(D, qs, kv):
+    clean = attn_case(D, 2, 4, 64, qs, [max(kv, n) for n in qs], seed=23)
+    c = dict(clean, q=clean["q"].clone())
+    T, Hq, _ = c["q"].shape
+    poisoned = np.zeros((T, Hq), bool)
+    poisoned[0, 1] = poisoned[T - 1, 6] = True
+    c["q"][0, 1, 3] = c["q"][T - 1, 6, D - 1] = float("nan")
+    lse = torch.zeros(T, Hq, device=DEV)
+    out = moe().moe_kv4_attention(*attn_args(c), scale=0.1, lse=lse)
+    check_poisoned(c, clean, out, lse, poisoned, 64, 0.1)
+
+
+@pytest.mark.parametrize("kv", [100, 3000])
+@pytest.mark.parametrize("D,qs", KERNELS)
+def test_a_key_that_is_not_a_number_answers_with_none(D, qs, kv):
+    """One block of one key of one head: all rows of that sequence and head see it."""
+    clean = attn_case(D, 2, 4, 64, qs, [max(kv, n) for n in qs], seed=24)
+    c = dict(clean, pool=clean["pool"].copy())
+    T, Hq, _ = c["q"].shape
+    oa.sections(c["pool"][c["table"][1, 0], 1], 64, D)[1][7, 2] = 0x7F
+    poisoned = np.zeros((T, Hq), bool)
+    poisoned[c["starts"][1]:c["starts"][2], 4:] = True
+    lse = torch.zeros(T, Hq, device=DEV)
+    out = moe().moe_kv4_attention(*attn_args(c), scale=0.1, lse=lse)
+    check_poisoned(c, clean, out, lse, poisoned, 64, 0.1)
