@@ -55,10 +55,12 @@
  *    permutation, reported as MOE_ERR_INVALID_ARG by moe_sync_status()),
  *    combine rows outside [0, T*k) (skipped), group offsets (clamped), and
  *    the pages, slots, rows and positions of the cache calls (see there).
- *  - The first call on each device that launches a permutation or a grouped
- *    GEMM looks up the device error word (cudaGetSymbolAddress) and sets
- *    kernel attributes; make such a call once before capturing any of them
- *    into a CUDA graph yourself (moe_forward_graph_create does it for you).
+ *  - The first call on each device that launches a permutation, a grouped
+ *    GEMM or a cache call looks up the device error word
+ *    (cudaGetSymbolAddress) and sets kernel attributes; make such a call (for
+ *    attention: of the same head size and about the same numbers of rows)
+ *    once before capturing any of them into a CUDA graph yourself
+ *    (moe_forward_graph_create does it for you).
  *  - Inputs are assumed finite; NaN / Inf inputs give unspecified results.
  *  - T = 0 (no tokens) is a valid no-op returning MOE_OK.
  */

@@ -2,6 +2,7 @@
 // the device error word of the bounded waits, and the wait time-out hook.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 
@@ -30,33 +31,35 @@ int check_launch() {
 }
 
 int num_sms() {
-  static int cache[64] = {0};
+  static std::atomic<int> cache[64];  // a racing first call stores the same number
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-  if (cache[dev] == 0) {
-    int n = 0;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    cache[dev] = n;
+    cache[dev].store(n, std::memory_order_relaxed);
   }
-  return cache[dev];
+  return n;
 }
 
 unsigned long long wait_timeout_ns() { return g_timeout_ns; }
 
 unsigned int* device_error_word() {
-  static unsigned int* cache[64] = {nullptr};
+  static std::atomic<unsigned int*> cache[64];  // a racing first call stores the same address
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
-  if (cache[dev] == nullptr) {
+  unsigned int* word = cache[dev].load(std::memory_order_relaxed);
+  if (word == nullptr) {
     void* p = nullptr;
     cudaError_t e = cudaGetSymbolAddress(&p, g_err_word);
     if (e != cudaSuccess) {
       set_cuda_error(e);
       return nullptr;
     }
-    cache[dev] = static_cast<unsigned int*>(p);
+    word = static_cast<unsigned int*>(p);
+    cache[dev].store(word, std::memory_order_relaxed);
   }
-  return cache[dev];
+  return word;
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {

@@ -10,6 +10,8 @@
 // boundary and the record a multiple of 16 bytes.
 #pragma once
 
+#include <atomic>
+
 #include "nvfp4.cuh"
 
 namespace moe {
@@ -38,6 +40,24 @@ inline int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int s
   if (e != cudaSuccess) {
     set_cuda_error(e);
     return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+// Lets a kernel use `bytes` of shared memory on the current device; `set` is the
+// kernel's own, by device.  Calls of several threads may come here at once: each
+// sets the same value.
+template <class... Params>
+inline int allow_smem(void (*kernel)(Params...), int bytes, std::atomic<bool> (&set)[64]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
+  if (!set[dev].load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) {
+      set_cuda_error(e);
+      return MOE_ERR_CUDA;
+    }
+    set[dev].store(true, std::memory_order_relaxed);
   }
   return MOE_OK;
 }

@@ -579,17 +579,8 @@ int launch_rows16(const AttnParams& p, cudaStream_t s) {
   // half records per warp: two at least (a unit's keys and values)
   const int slots = std::min(kMaxSlots / kWarps, (kSmem / kGroups - head) / (kWarps * half));
   const int smem = kGroups * (head + kWarps * slots * half);
-  static bool set[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  if (!set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_rows16_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) {
-      set_cuda_error(e);
-      return MOE_ERR_CUDA;
-    }
-    set[dev] = true;
-  }
+  static std::atomic<bool> set[64];
+  MOE_TRY(allow_smem(attn_rows16_kernel, kSmem, set));
   return launch_after(attn_rows16_kernel, dim3(p.blocks / kGroups), kThreads, smem, s, p, slots);
 }
 

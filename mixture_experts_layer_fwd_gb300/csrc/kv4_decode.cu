@@ -649,18 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const AttnPara
 
 template <bool HERE>
 int launch(const AttnParams& p, int k_slots, int v_slots, int smem, cudaStream_t s) {
-  static bool set[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  if (!set[dev]) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(attn_decode_kernel<HERE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) {
-      set_cuda_error(e);
-      return MOE_ERR_CUDA;
-    }
-    set[dev] = true;
-  }
+  static std::atomic<bool> set[64];
+  MOE_TRY(allow_smem(attn_decode_kernel<HERE>, kSmem, set));
   // with a schedule kernel in front, this one may begin under it
   if (!HERE) return launch_after(attn_decode_kernel<HERE>, dim3(p.blocks), kThreads, smem, s, p, k_slots, v_slots);
   attn_decode_kernel<HERE><<<p.blocks, kThreads, smem, s>>>(p, k_slots, v_slots);

@@ -549,18 +549,8 @@ int launch(const AttnParams& p, cudaStream_t s) {
   const int all = std::min(2 * kMaxSlots, C::RING / half);
   const int k_slots = (all + 1) / 2, v_slots = all / 2;
   const int smem = C::RING0 + all * half;
-  static bool set[64] = {false};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return MOE_ERR_CUDA;
-  if (!set[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(attn_tiles_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               C::RING0 + C::RING);
-    if (e != cudaSuccess) {
-      set_cuda_error(e);
-      return MOE_ERR_CUDA;
-    }
-    set[dev] = true;
-  }
+  static std::atomic<bool> set[64];
+  MOE_TRY(allow_smem(attn_tiles_kernel<D>, C::RING0 + C::RING, set));
   return launch_after(attn_tiles_kernel<D>, dim3(p.blocks), kThreads, smem, s, p, k_slots, v_slots);
 }
 

@@ -4,7 +4,9 @@ library's cache calls on them.
 
 Everything stays on the device: a step's new tokens are placed by
 moe_kv_extend, written by moe_qk_norm_rope and read by moe_kv4_attention, all
-on the current stream, without a host read.
+on the current stream, without a host read.  extend, fork and free take their
+numbers from the host, so a CUDA graph holds attend() calls or the library's calls
+on index tensors, not those three.
 """
 from __future__ import annotations
 

@@ -250,3 +250,80 @@ def test_a_key_that_is_not_a_number_answers_with_none(D, qs, kv):
     lse = torch.zeros(T, Hq, device=DEV)
     out = moe().moe_kv4_attention(*attn_args(c), scale=0.1, lse=lse)
     check_poisoned(c, clean, out, lse, poisoned, 64, 0.1)
+
+
+# --------------------------------------------------------- graphs and threads
+@pytest.mark.parametrize("D,qs", KERNELS)
+def test_a_step_in_a_graph(D, qs):
+    """Pages for new tokens, norms with the write, attention, a fork, a release and a compaction, replayed on new inputs."""
+    m = moe()
+    B, T, Hq, Hkv, P = len(qs), sum(qs), 8, 2, 32
+    M, N, S = 20, 20 * 45, len(qs) + 1
+    g = torch.full((Hkv,), 5.0 / 2688, device=DEV)
+    gen = torch.Generator(DEV).manual_seed(3)
+    r = lambda h: torch.randn(T, h, D, generator=gen, device=DEV).bfloat16()  # noqa: E731
+    q, k, v = r(Hq), r(Hkv), r(Hkv)
+    a = torch.arange(900, device=DEV).unsqueeze(1) * 1e4 ** (-torch.arange(0, D, 2, device=DEV) / D)
+    cs = torch.cat((a.cos(), a.sin()), 1).float().contiguous()
+    offsets = dev(np.cumsum([0] + qs + [0]), I32)
+    table, lens, refs = torch.full((S, M), -1, dtype=I32, device=DEV), dev([0] * S, I32), dev([0] * N, I32)
+    pool = torch.zeros(1, N, Hkv, oa.record_bytes(P, D), dtype=torch.uint8, device=DEV)
+    src, dst = dev([0], I32), dev([B], I32)
+
+    def step():
+        e = m.moe_kv_extend(offsets, T, table, lens, refs, P, inplace=True)
+        y, _ = m.moe_qk_norm_rope(q, k, cs, e["pos"], v=v, pool=pool[0], g_k=g, g_v=g, slots=e["slots"])
+        out = m.moe_kv4_attention(y, pool[0], g, g, offsets, lens, table)
+        m.moe_kv_fork(src, dst, table, lens, refs, pool, P, inplace=True)
+        m.moe_kv_free(dst, table, lens, refs, P, inplace=True)
+        m.moe_kv_compact(table, refs, pool, inplace=True)
+        return out
+
+    fresh = [t.clone() for t in (table, lens, refs, pool)]
+
+    def reset():
+        for t, f in zip((table, lens, refs, pool), fresh):
+            t.copy_(f)
+
+    want = [step().clone() for _ in range(2)]  # the second step's context is the first one's tokens and its own
+    held = [t.clone() for t in (table, lens, refs, pool)]
+    reset()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    reset()
+    for y in want:
+        graph.replay()
+        assert torch.equal(out, y)
+    for t, h in zip((table, lens, refs, pool), held):
+        assert torch.equal(t, h)
+    assert m.moe_sync_status() == 0
+
+
+def test_calls_of_several_threads():
+    """Each on a stream of its own, all kernels at once."""
+    m = moe()
+    cases = [attn_case(D, 2, 4, 64, qs, [300] * len(qs), seed=26) for D, qs in KERNELS]
+    args = [attn_args(c) for c in cases]
+    want = [m.moe_kv4_attention(*a, scale=0.1) for a in args]
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(n):
+        try:
+            s = torch.cuda.Stream()
+            for i in range(len(args)):
+                j = (i + n) % len(args)
+                got[n, j] = m.moe_kv4_attention(*args[j], scale=0.1, stream=s)
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(n,)) for n in range(6)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and all(torch.equal(y, want[j]) for (_, j), y in got.items())
+    assert m.moe_sync_status() == 0
