@@ -44,6 +44,24 @@ inline int launch_after(void (*kernel)(Params...), dim3 grid, int threads, int s
   return MOE_OK;
 }
 
+// Pairs of fp32 in one register pair; each half is one IEEE operation.
+DEVINL uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+DEVINL void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+DEVINL uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // Lets a kernel use `bytes` of shared memory on the current device; `set` is the
 // kernel's own, by device.  Calls of several threads may come here at once: each
 // sets the same value.

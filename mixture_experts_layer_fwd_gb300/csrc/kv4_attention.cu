@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
   constexpr int KS = D / 16;  // k steps of S
   constexpr int LD = D / 4;   // values of a key per lane (S), of a row of O per lane
   constexpr int NT = D / 8;   // column tiles of O
-  constexpr int W = D / 64;   // words of a value row per lane
   extern __shared__ __align__(128) uint8_t smem[];
   const int rec = record_bytes(p.P, D), hb = rec / 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -364,25 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
         for (int kt = 0; kt < 4; ++kt) {
           s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.0f;
           const int tok = t0 + 8 * kt + (g ^ ((g >> 1) & 1));
-          uint32_t w[LD / 8];
-          uint32_t sb[2];
-          if (LD == 32) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kc + tok * (D / 2) + c4 * 16);
-            w[0] = v.x, w[1] = v.y, w[2 % (LD / 8)] = v.z, w[3 % (LD / 8)] = v.w;
-            const uint32_t f = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(ks + tok * (D / 16) + 2 * c4));
-            sb[0] = __byte_perm(f, f, 0x1010);
-            sb[1] = __byte_perm(f, f, 0x3232);
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kc + tok * (D / 2) + c4 * 8);
-            w[0] = v.x, w[1] = v.y;
-            const uint32_t f = e4m3x2_to_f16x2(ks[tok * (D / 16) + c4]);
-            sb[0] = sb[1] = __byte_perm(f, f, 0x1010);
-          }
+          const uint2 v = *reinterpret_cast<const uint2*>(kc + tok * (D / 2) + c4 * 8);
+          const uint32_t w[LD / 8] = {v.x, v.y};
+          const uint32_t two = e4m3x2_to_f16x2(ks[tok * (D / 16) + c4]);
+          const uint32_t f = __byte_perm(two, two, 0x1010);
 #pragma unroll
           for (int j = 0; j < LD / 8; ++j) {
             uint32_t h[4];
             e2m1x8(w[j], h);
-            const uint32_t f = sb[j >> 1];
 #pragma unroll
             for (int q = 0; q < 4; ++q) h[q] = hmul2(h[q], f);
             mma_f16(s[kt], qa[2 * j], h[0], h[1]);
@@ -459,38 +447,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_rows16_kernel(const AttnPara
         }
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-          uint32_t wa[2][W], wb[2][W], f[2];
+          uint32_t wa[2], wb[2], f[2];
 #pragma unroll
           for (int pr = 0; pr < 2; ++pr) {
             const int ta = t0 + 16 * kb + 8 * pr + ((2 * c4) ^ (c4 & 1)), tb = ta ^ 1;
-            const uint32_t sa = vs[ta * (D / 16) + (D == 128 ? g : g >> 1)];
-            const uint32_t sb = vs[tb * (D / 16) + (D == 128 ? g : g >> 1)];
+            const uint32_t sa = vs[ta * (D / 16) + (g >> 1)];
+            const uint32_t sb = vs[tb * (D / 16) + (g >> 1)];
             f[pr] = e4m3x2_to_f16x2(sa | (sb << 8));
-            if (W == 2) {
-              const uint2 va = *reinterpret_cast<const uint2*>(vc + ta * (D / 2) + 8 * g);
-              const uint2 vb = *reinterpret_cast<const uint2*>(vc + tb * (D / 2) + 8 * g);
-              wa[pr][0] = va.x, wa[pr][W - 1] = va.y, wb[pr][0] = vb.x, wb[pr][W - 1] = vb.y;
-            } else {
-              wa[pr][0] = *reinterpret_cast<const uint32_t*>(vc + ta * (D / 2) + 4 * g);
-              wb[pr][0] = *reinterpret_cast<const uint32_t*>(vc + tb * (D / 2) + 4 * g);
-            }
+            wa[pr] = *reinterpret_cast<const uint32_t*>(vc + ta * (D / 2) + 4 * g);
+            wb[pr] = *reinterpret_cast<const uint32_t*>(vc + tb * (D / 2) + 4 * g);
           }
 #pragma unroll
-          for (int j = 0; j < W; ++j)
+          for (int odd = 0; odd < 2; ++odd) {
+            uint32_t b[2][4];
 #pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {
-              uint32_t b[2][4];
+            for (int pr = 0; pr < 2; ++pr) {
+              e2m1x8(odd ? ((wa[pr] >> 4) & 0x0F0F0F0Fu) | (wb[pr] & 0xF0F0F0F0u)
+                         : (wa[pr] & 0x0F0F0F0Fu) | ((wb[pr] << 4) & 0xF0F0F0F0u),
+                     b[pr]);
 #pragma unroll
-              for (int pr = 0; pr < 2; ++pr) {
-                e2m1x8(odd ? ((wa[pr][j] >> 4) & 0x0F0F0F0Fu) | (wb[pr][j] & 0xF0F0F0F0u)
-                           : (wa[pr][j] & 0x0F0F0F0Fu) | ((wb[pr][j] << 4) & 0xF0F0F0F0u),
-                       b[pr]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) b[pr][q] = hmul2(b[pr][q], f[pr]);
-              }
-#pragma unroll
-              for (int q = 0; q < 4; ++q) mma_f16(o[8 * j + 2 * q + odd], pa[kb], b[0][q], b[1][q]);
+              for (int q = 0; q < 4; ++q) b[pr][q] = hmul2(b[pr][q], f[pr]);
             }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) mma_f16(o[2 * q + odd], pa[kb], b[0][q], b[1][q]);
+          }
         }
       }
       __syncwarp();

@@ -54,22 +54,10 @@ DEVINL void e2m1x8(uint32_t w, uint32_t (&h)[4]) {
       : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
       : "r"(w));
 }
-// Pairs of fp32 in one register pair.
-DEVINL uint64_t pair(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-DEVINL void unpair(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-DEVINL uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
+// 16 bytes to shared memory, without a memory clobber: loads of record bytes may
+// move past stores to operand tiles.
+DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
 }
 
 // A query row's power of two and softmax scale, from its largest magnitude (as
@@ -150,15 +138,15 @@ DEVINL void tile_units(const AttnParams& p, const Seq& s, int tile, int unit, in
   u0 = min(lo / unit, u1 - 1);
 }
 
-// Largest i in [0, n) with a[i] <= x (a ascending, a[0] <= x), by a whole warp.
-template <class T>
-DEVINL int warp_find(const T* a, int n, long long x, long long factor) {
+// Largest i in [0, n) with at(i) <= x (at ascending, at(0) <= x), by a whole warp.
+template <class At>
+DEVINL int warp_find(int n, long long x, At at) {
   int lo = 0, hi = n;
   const int lane = threadIdx.x & 31;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int i = lo + lane * step;
-    const bool le = i < hi && a[i] * factor <= x;
+    const bool le = i < hi && at(i) <= x;
     const int k = __popc(__ballot_sync(0xFFFFFFFFu, le));
     lo += (k - 1) * step;
     hi = min(hi, lo + step);
@@ -185,23 +173,13 @@ DEVINL Cursor cursor_at(const AttnParams& p, int unit, long long x) {
   Cursor c;
   // largest b whose first unit is at or before x: sequences without queries
   // take no room, so step over tile_base to the sequence that owns the tile
-  int lo = 0, hi = p.B;
-  const int lane = threadIdx.x & 31;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int i = lo + lane * step;
-    const bool le = i < hi && p.unit_sum[p.tile_base[i]] * p.Hkv <= x;
-    const int k = __popc(__ballot_sync(0xFFFFFFFFu, le));
-    lo += (k - 1) * step;
-    hi = min(hi, lo + step);
-  }
-  c.b = lo;
-  const int t0 = p.tile_base[lo], t1 = p.tile_base[lo + 1];
+  c.b = warp_find(p.B, x, [&](int i) { return p.unit_sum[p.tile_base[i]] * p.Hkv; });
+  const int t0 = p.tile_base[c.b], t1 = p.tile_base[c.b + 1];
   const long long base = p.unit_sum[t0], w = p.unit_sum[t1] - base;
   long long r = x - base * p.Hkv;
   c.h = static_cast<int>(r / w);
   r -= c.h * w;
-  c.tile = warp_find(p.unit_sum + t0, t1 - t0, base + r, 1);
+  c.tile = warp_find(t1 - t0, base + r, [&](int i) { return p.unit_sum[t0 + i]; });
   c.s = load_seq(p, c.b);
   cursor_item<ROWS>(p, unit, c);
   c.u = c.u0 + static_cast<int>(base + r - p.unit_sum[t0 + c.tile]);

@@ -89,9 +89,6 @@ static_assert(O0 + 4 * kRows <= TMEM_COLS, "tensor memory");
 DEVINL void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b));
 }
-DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
-}
 // 16 lanes of tensor memory by 16 columns as matrix fragments: register 4 c + 2 r + e
 // of a thread is lane 8 r + (thread / 4), column 8 c + 2 (thread % 4) + e.
 DEVINL void tmem_ld_16x256b_x2(uint32_t addr, uint32_t* r) {

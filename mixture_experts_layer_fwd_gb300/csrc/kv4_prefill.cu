@@ -65,11 +65,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 3328, "between the operand tiles and the ring");
 
-DEVINL void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  // no memory clobber: loads of record bytes may move past stores to operand tiles
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d));
-}
-
 // Half h of a query row to fp16 in the swizzled tile, read in one round trip;
 // the two threads of a row exchange their largest magnitudes.  Returns the
 // softmax scale of the row in log2 units (> 0).

@@ -19,6 +19,8 @@
 namespace moe {
 namespace {
 
+using kv4::add2, kv4::fma2, kv4::pair, kv4::unpair;
+
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;  // head groups in flight per warp
 
@@ -41,26 +43,10 @@ struct NormParams {
   unsigned int* err;
 };
 
-// Packed fp32 pairs: each half one IEEE rounding.
-DEVINL uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-DEVINL void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
 // a * b + (-0): the product rounded once, with its sign.  The zero comes from
 // the kernel's parameters because the assembler turns a constant one back into
 // a product and then contracts packed products with sums.
-DEVINL uint64_t mul2(uint64_t a, uint64_t b, uint64_t neg_zero) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(neg_zero));
-  return r;
-}
-DEVINL uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+DEVINL uint64_t mul2(uint64_t a, uint64_t b, uint64_t neg_zero) { return fma2(a, b, neg_zero); }
 
 // A lane's 8 consecutive values (D/8 lanes per head) as pairs (0,2) (1,3) (4,6)
 // (5,7): the sum's neighbours and an interleaved rotation's partners face each
@@ -71,16 +57,16 @@ struct Eight {
 DEVINL Eight from_bf16(const uint4& u) {
   auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
   auto hi = [](uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); };
-  return Eight{{pack2(lo(u.x), lo(u.y)), pack2(hi(u.x), hi(u.y)), pack2(lo(u.z), lo(u.w)), pack2(hi(u.z), hi(u.w))}};
+  return Eight{{pair(lo(u.x), lo(u.y)), pair(hi(u.x), hi(u.y)), pair(lo(u.z), lo(u.w)), pair(hi(u.z), hi(u.w))}};
 }
 DEVINL Eight from_float(const float (&x)[8]) {
-  return Eight{{pack2(x[0], x[2]), pack2(x[1], x[3]), pack2(x[4], x[6]), pack2(x[5], x[7])}};
+  return Eight{{pair(x[0], x[2]), pair(x[1], x[3]), pair(x[4], x[6]), pair(x[5], x[7])}};
 }
 DEVINL void to_float(const Eight& e, float (&x)[8]) {
-  unpack2(e.v[0], x[0], x[2]);
-  unpack2(e.v[1], x[1], x[3]);
-  unpack2(e.v[2], x[4], x[6]);
-  unpack2(e.v[3], x[5], x[7]);
+  unpair(e.v[0], x[0], x[2]);
+  unpair(e.v[1], x[1], x[3]);
+  unpair(e.v[2], x[4], x[6]);
+  unpair(e.v[3], x[5], x[7]);
 }
 DEVINL uint4 to_bf16(const Eight& e) {
   float x[8];
@@ -94,8 +80,8 @@ DEVINL float head_sum(const Eight& e, uint64_t nz) {
   const uint64_t a = add2(mul2(e.v[0], e.v[0], nz), mul2(e.v[1], e.v[1], nz));  // (0+1, 2+3)
   const uint64_t b = add2(mul2(e.v[2], e.v[2], nz), mul2(e.v[3], e.v[3], nz));
   float a0, a1, b0, b1;
-  unpack2(a, a0, a1);
-  unpack2(b, b0, b1);
+  unpair(a, a0, a1);
+  unpair(b, b0, b1);
   float t = __fadd_rn(__fadd_rn(a0, a1), __fadd_rn(b0, b1));
 #pragma unroll
   for (int o = 1; o < D / 8; o <<= 1) t = __fadd_rn(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
@@ -163,7 +149,7 @@ DEVINL void heads_step(const NormParams& p, const Lane<D, PAIRS>& L, const uint1
     const int h = h0 + u * HPW + L.sub;
     Eight x = from_bf16(raw[u]);
     if (norm) {
-      const uint64_t rr = pack2(r[u], r[u]);
+      const uint64_t rr = pair(r[u], r[u]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x.v[i] = mul2(mul2(x.v[i], rr, nz), w.v[i], nz);
     }
