@@ -497,7 +497,8 @@ int moe_graph_destroy(void* graph);
  * other: key codes [page_size][D/2], key scales [page_size][D/16], value
  * codes, value scales; page_size * D * 9 / 8 bytes.  Codes and scales are
  * NVFP4 along D with one given fp32 global scale per kv head (g_k, g_v
- * [Hkv]).  Token slot s lies in page s / page_size at offset s % page_size.
+ * [Hkv], finite and not 0: 1 for a head that is all zeros).  A block of 16 that
+ * holds a NaN gets a scale of NaN.  Token slot s lies in page s / page_size at offset s % page_size.
  * page_size is 32, 64 or 128 and D 64 or 128.  The pool is 16-byte aligned.
  *
  * Sequences: table int32 [rows][max_pages] holds the page of tokens

@@ -88,13 +88,21 @@ DEVINL float head_sum(const Eight& e, uint64_t nz) {
   return t;
 }
 
+// Keeps a NaN: the scale of its block is one too, so that a key that is not a
+// number does not turn into one.
+DEVINL float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The lane's 8 values (half a block of 16; lanes 2j and 2j+1 share it) as
 // NVFP4 with global scale g: returns the 8 codes, `s` the block's scale byte.
 DEVINL uint32_t quantise8(const float (&v)[8], float g, uint32_t& s) {
   float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(v[i]));
-  amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+  for (int i = 0; i < 8; ++i) amax = max_nan(amax, fabsf(v[i]));
+  amax = max_nan(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   s = e4m3_encode_satfinite(__fdiv_rn(amax, __fmul_rn(6.0f, g)));
   const float denom = __fmul_rn(e4m3_decode(s), g);
   const float r = denom != 0.0f ? __frcp_rn(denom) : 0.0f;

@@ -327,3 +327,32 @@ def test_calls_of_several_threads():
         t.join()
     assert not errors and all(torch.equal(y, want[j]) for (_, j), y in got.items())
     assert m.moe_sync_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_key_that_is_not_a_number_is_stored_as_none(D):
+    """Its blocks of 16 have scales that are not a number, all other bytes are as without it."""
+    m, T, Hkv, P = moe(), 9, 3, 32
+    gen = torch.Generator(DEV).manual_seed(31)
+    q, k, v = (torch.randn(T, h, D, generator=gen, device=DEV).bfloat16() for h in (4, Hkv, Hkv))
+    w, g = torch.ones(D, dtype=torch.bfloat16, device=DEV), torch.full((Hkv,), 0.002, device=DEV)
+    slots = torch.arange(T, device=DEV) + 20
+
+    def write():
+        pool = torch.zeros(1, Hkv, oa.record_bytes(P, D), dtype=torch.uint8, device=DEV)
+        m.moe_qk_norm_rope(q, k, wq=w, wk=w, v=v, pool=pool, g_k=g, g_v=g, slots=slots)
+        return [s.copy() for h in range(Hkv) for s in oa.sections(pool[0, h].cpu().numpy(), P, D)]
+
+    clean = write()
+    k[4, 1, 5] = v[6, 2, 37] = float("nan")  # a norm spreads it over the head
+    got = write()
+    at = {(4 * 1 + 1, 24): range(D // 16), (4 * 2 + 3, 26): [2]}
+    for i, (a, b) in enumerate(zip(clean, got)):
+        other = np.ones(P, bool)
+        for (section, token), blocks in at.items():
+            if i == section:
+                assert [int(x) & 0x7F for x in b[token][list(blocks)]] == [0x7F] * len(blocks)
+                assert all(b[token][j] == a[token][j] for j in range(D // 16) if j not in blocks)
+            if i in (section, section - 1):
+                other[token] = False
+        assert np.array_equal(a[other], b[other])
