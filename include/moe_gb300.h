@@ -574,6 +574,14 @@ int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* table_in, cons
                   int32_t* table_out, int32_t* lens_out, int32_t* refs_out, long long* slots, int32_t* pos,
                   void* ws, size_t ws_bytes, void* stream);
 
+/* The same, and kv_lens int32 [rows] (another array than lens, or NULL): the
+ * lengths for this step's attention, lens_out but 0 for a row that failed, so
+ * that the queries of its tokens see no keys. */
+int moe_kv_extend_ex(const int32_t* q_offsets, int T, const int32_t* table_in, const int32_t* lens_in,
+                     const int32_t* refs_in, int rows, int max_pages, int num_pages, int page_size,
+                     int32_t* table_out, int32_t* lens_out, int32_t* refs_out, long long* slots, int32_t* pos,
+                     int32_t* kv_lens, void* ws, size_t ws_bytes, void* stream);
+
 /* Row dst[i] becomes a fork of row src[i] (n pairs, int32): full pages are
  * shared, the partial page is copied to a free one in every layer.  The pools
  * of the layers are layer_stride bytes apart, a page is page_bytes long

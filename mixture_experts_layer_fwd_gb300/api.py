@@ -758,14 +758,24 @@ def _like(out, name, t, inplace, stream):
 
 
 def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
-                  page_size: int, inplace: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+                  page_size: int, inplace: bool = False, out: Optional[dict] = None,
+                  kv_lens: Optional[torch.Tensor] = None, stream=None) -> dict:
     """Room for new tokens: row r gets tokens q_offsets[r] .. q_offsets[r+1]
     (int32 [rows + 1], T tokens in all).  Returns dict(table, lens, refs,
     slots int64 [T], pos int32 [T]); inplace=True writes the state back into
-    the arguments, `out` may hold any of the outputs."""
+    the arguments, `out` may hold any of the outputs.  kv_lens int32 [rows],
+    where given, gets the lengths for this step's attention: 0 for a row that
+    found no room."""
     S, M, N = _kv_state(table, refs, lens)
     dev = table.device
-    _dev(q_offsets, "q_offsets", dtype=torch.int32, shape=(S + 1,), device=dev)
+    try:
+        di = table.get_device()
+        ok = _is(q_offsets, _I32, (S + 1,), di) and (kv_lens is None or _is(kv_lens, _I32, (S,), di))
+    except AttributeError:
+        ok = False
+    if not ok:
+        _dev(q_offsets, "q_offsets", dtype=torch.int32, shape=(S + 1,), device=dev)
+        _opt(kv_lens, "kv_lens", dtype=torch.int32, shape=(S,), device=dev)
     o = out or {}
     r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
              lens=_like(o.get("lens"), "lens", lens, inplace, stream),
@@ -781,9 +791,9 @@ def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: to
             r["pos"].zero_()
     lib = load()
     ws = _empty(lib.moe_kv_pages_workspace_size(N, S), torch.uint8, dev, stream)
-    check(lib.moe_kv_extend(_ptr(q_offsets), T, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
-                            _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _ptr(r["slots"]), _ptr(r["pos"]),
-                            _ptr(ws), ws.numel(), _raw_stream(stream, table)), "moe_kv_extend")
+    check(lib.moe_kv_extend_ex(_ptr(q_offsets), T, _ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size,
+                               _ptr(r["table"]), _ptr(r["lens"]), _ptr(r["refs"]), _ptr(r["slots"]), _ptr(r["pos"]),
+                               _ptr(kv_lens), _ptr(ws), ws.numel(), _raw_stream(stream, table)), "moe_kv_extend")
     return r
 
 

@@ -218,7 +218,8 @@ __global__ void __launch_bounds__(kPlan) extend_plan_kernel(State s, const int32
   if (threadIdx.x == 0) w.count[0] = found;
 }
 
-__global__ void extend_apply_kernel(State s, int T, Plan w, long long* slots, int32_t* pos, unsigned int* err) {
+__global__ void extend_apply_kernel(State s, int T, Plan w, long long* slots, int32_t* pos, int32_t* kv_lens,
+                                    unsigned int* err) {
   kv4::wait_for_previous();
   const int r = blockIdx.x;
   if (r == s.S) {  // tokens of no row: in front of the first one's and behind the last one's
@@ -252,7 +253,10 @@ __global__ void extend_apply_kernel(State s, int T, Plan w, long long* slots, in
     pos[t] = at;
   }
   __syncthreads();
-  if (threadIdx.x == 0 && ok && t1 > t0) s.lens[r] = len + (t1 - t0);
+  if (threadIdx.x == 0) {
+    if (ok && t1 > t0) s.lens[r] = len + (t1 - t0);
+    if (kv_lens) kv_lens[r] = ok ? len + max(0, t1 - t0) : 0;
+  }
 }
 
 // -------------------------------------------------------------------- fork
@@ -487,12 +491,21 @@ extern "C" int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* tab
                              const int32_t* refs_in, int rows, int max_pages, int num_pages, int page_size,
                              int32_t* table_out, int32_t* lens_out, int32_t* refs_out, long long* slots, int32_t* pos,
                              void* ws, size_t ws_bytes, void* stream) {
+  return moe_kv_extend_ex(q_offsets, T, table_in, lens_in, refs_in, rows, max_pages, num_pages, page_size, table_out,
+                          lens_out, refs_out, slots, pos, nullptr, ws, ws_bytes, stream);
+}
+
+extern "C" int moe_kv_extend_ex(const int32_t* q_offsets, int T, const int32_t* table_in, const int32_t* lens_in,
+                                const int32_t* refs_in, int rows, int max_pages, int num_pages, int page_size,
+                                int32_t* table_out, int32_t* lens_out, int32_t* refs_out, long long* slots, int32_t* pos,
+                                int32_t* kv_lens, void* ws, size_t ws_bytes, void* stream) {
   State s{table_in, lens_in, refs_in, table_out, lens_out, refs_out, rows, max_pages, num_pages, page_size};
   if (T < 0) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_state(s));
   if (rows == 0) return carry_refs(s, stream);
   if (!q_offsets || !lens_in || !lens_out || !aligned(q_offsets, 4)) return MOE_ERR_INVALID_ARG;
   if (T > 0 && (!slots || !pos || !aligned(slots, 8) || !aligned(pos, 4))) return MOE_ERR_INVALID_ARG;
+  if (kv_lens && (kv_lens == lens_out || kv_lens == lens_in || !aligned(kv_lens, 4))) return MOE_ERR_INVALID_ARG;
   MOE_TRY(check_ws(ws, ws_bytes, num_pages, rows));
   unsigned int* err = device_error_word();
   if (!err) return MOE_ERR_CUDA;
@@ -500,7 +513,7 @@ extern "C" int moe_kv_extend(const int32_t* q_offsets, int T, const int32_t* tab
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   extend_plan_kernel<<<1 + carry_blocks(s), kPlan, 0, st>>>(s, q_offsets, T, w, err);
   MOE_TRY(check_launch());
-  return kv4::launch_after(extend_apply_kernel, dim3(rows + 1), 128, 0, st, s, T, w, slots, pos, err);
+  return kv4::launch_after(extend_apply_kernel, dim3(rows + 1), 128, 0, st, s, T, w, slots, pos, kv_lens, err);
 }
 
 extern "C" int moe_kv_fork(const int32_t* src, const int32_t* dst, int n, const int32_t* table_in,

@@ -10,6 +10,7 @@ on index tensors, not those three.
 """
 from __future__ import annotations
 
+import itertools
 from typing import List, Optional, Sequence
 
 import torch
@@ -33,13 +34,13 @@ class KV4Cache:
         self.pool = torch.empty(layers, num_pages, Hkv, page_size * D * 9 // 8, dtype=torch.uint8, device=dev)
         self.table = torch.full((rows, max_pages), -1, dtype=torch.int32, device=dev)
         self.lens = torch.zeros(rows, dtype=torch.int32, device=dev)
+        self.kv_lens = torch.zeros_like(self.lens)  # as the step's attention takes them
         self.refs = torch.zeros(num_pages, dtype=torch.int32, device=dev)
         # of the step that extend() made room for; None from the call on that moves
         # rows or pages, since its slots may be another row's after that
         self.q_offsets: Optional[torch.Tensor] = None
         self.slots: Optional[torch.Tensor] = None
         self.pos: Optional[torch.Tensor] = None
-        self.kv_lens: Optional[torch.Tensor] = None
 
     def _rows(self, rows: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
@@ -49,18 +50,14 @@ class KV4Cache:
         and kv_lens for this step.  A row that finds no free page, or has no room
         in its table row, keeps its length; moe_sync_status() reports it, and the
         step's attention sees no keys for its tokens (zeros)."""
-        if len(counts) != self.lens.numel() or any(n < 0 for n in counts):
-            raise ValueError(f"counts: expected {self.lens.numel()} numbers of new tokens, one per row, got {list(counts)}")
-        offsets = [0]
-        for n in counts:
-            offsets.append(offsets[-1] + int(n))
-        T = offsets[-1]
+        rows = self.table.shape[0]
+        if len(counts) != rows or min(counts, default=0) < 0:
+            raise ValueError(f"counts: expected {rows} numbers of new tokens, one per row, got {list(counts)}")
+        offsets = [0, *itertools.accumulate(map(int, counts))]
         q_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
-        r = api.moe_kv_extend(q_offsets, T, self.table, self.lens, self.refs, self.page_size, inplace=True)
-        self.q_offsets, self.slots, self.pos, self.kv_lens = q_offsets, r["slots"], r["pos"], self.lens
-        if T > 0:  # a row's first new token has no slot: none of them has
-            first = self.slots.index_select(0, q_offsets[:-1].clamp(max=T - 1))
-            self.kv_lens = self.lens.masked_fill(first < 0, 0)
+        r = api.moe_kv_extend(q_offsets, offsets[-1], self.table, self.lens, self.refs, self.page_size, inplace=True,
+                              kv_lens=self.kv_lens)
+        self.q_offsets, self.slots, self.pos = q_offsets, r["slots"], r["pos"]
 
     def attend(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
                wq: Optional[torch.Tensor] = None, wk: Optional[torch.Tensor] = None, eps: float = 1e-6,
@@ -78,16 +75,16 @@ class KV4Cache:
 
     def fork(self, src: Sequence[int], dst: Sequence[int]) -> None:
         """Empty rows dst continue as forks of rows src."""
-        self.q_offsets = self.slots = self.pos = self.kv_lens = None
+        self.q_offsets = self.slots = self.pos = None
         api.moe_kv_fork(self._rows(src), self._rows(dst), self.table, self.lens, self.refs, self.pool, self.page_size,
                         inplace=True)
 
     def free(self, rows: Sequence[int]) -> None:
         """Rows become empty."""
-        self.q_offsets = self.slots = self.pos = self.kv_lens = None
+        self.q_offsets = self.slots = self.pos = None
         api.moe_kv_free(self._rows(rows), self.table, self.lens, self.refs, self.page_size, inplace=True)
 
     def compact(self) -> torch.Tensor:
         """Moves the pages in use to the lowest ids; returns the new id of each page (-1: free)."""
-        self.q_offsets = self.slots = self.pos = self.kv_lens = None
+        self.q_offsets = self.slots = self.pos = None
         return api.moe_kv_compact(self.table, self.refs, self.pool, inplace=True)["remap"]

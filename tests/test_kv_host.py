@@ -110,6 +110,11 @@ def test_page_operations_host_checks(lib, name):
     assert lib.moe_kv_copy_pages(P(4104), 1, 64, 16, 4, A, A, 2, None) == INVALID
 
 
+def test_lengths_of_a_step_are_an_array_of_their_own(lib):
+    f = lambda lens_out, kv: lib.moe_kv_extend_ex(A, 2, A, A, A, 4, 2, 8, 64, A, lens_out, A, A, A, kv, A, 1 << 30, None)  # noqa: E731
+    assert f(P(8192), P(8192)) == INVALID and f(P(8192), A) == INVALID and f(A, P(4098)) == INVALID
+
+
 @pytest.mark.parametrize("name", ["extend", "fork", "free", "compact"])
 def test_page_operations_check_refs_of_a_table_without_rows(lib, name):
     """They are read 16 bytes at a time with no rows too."""
