@@ -372,3 +372,40 @@ def test_lengths_of_a_step_are_checked():
     kv = i(3) + 9
     o = m.moe_kv_extend(dev([0, 3, 3, 90], I32), 90, table, lens, refs, 32, kv_lens=kv)  # the third has no room
     assert m.moe_sync_status() == 1 and kv.tolist() == [3, 0, 0] and o["lens"].tolist() == [3, 0, 0]
+
+
+# ------------------------------------------------------------------- many forks
+def test_many_forks_and_rows_named_twice():
+    """More pairs than a block has threads, some with a destination that an earlier pair has named, in any order."""
+    m, P, S, n = moe(), 32, 5000, 3000
+    rng = np.random.default_rng(41)
+    s = oa.Pages([[-1] * 3 for _ in range(S)], [0] * S, [0] * 6000, P)
+    s.extend([int(x) for x in rng.integers(1, 90, 1500)] + [0] * (S - 1500))
+    src, dst = rng.integers(0, 1500, n), rng.permutation(np.arange(1500, S))[:n]
+    again = np.sort(rng.permutation(np.arange(1, n))[:400])
+    dst[again] = dst[rng.integers(0, again)]
+    dst[rng.integers(0, n, 30)] = rng.integers(-3, 1500, 30)  # in use, or none
+    _, first = np.unique(dst, return_index=True)
+    good = [int(i) for i in np.sort(first) if 1500 <= dst[i] < S]
+    table, lens, refs = state(s)
+    s.fork([int(src[i]) for i in good], [int(dst[i]) for i in good])
+    same(m.moe_kv_fork(dev(src, I32), dev(dst, I32), table, lens, refs, page_size=P), s)
+    assert m.moe_sync_status() == 1
+
+
+def test_as_many_forks_as_a_call_takes():
+    """65536 of a row of one full page.  Their check reads each pair a few times: some
+    thousand steps of a block, a millisecond with a factor of five to spare."""
+    m, n = moe(), 65536
+    i = lambda *s: torch.zeros(*s, dtype=I32, device=DEV)  # noqa: E731
+    table, lens, refs = i(n + 1, 1) - 1, i(n + 1), i(8)
+    table[0], lens[0], refs[0] = 0, 32, 1
+    src, dst = i(n), torch.arange(1, n + 1, dtype=I32, device=DEV)
+    t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    for _ in range(2):
+        t[0].record()
+        o = m.moe_kv_fork(src, dst, table, lens, refs, page_size=32)
+        t[1].record()
+    assert m.moe_sync_status() == 0
+    assert (o["table"] == 0).all() and (o["lens"] == 32).all() and o["refs"].tolist() == [n + 1] + [0] * 7
+    assert t[0].elapsed_time(t[1]) < 5
