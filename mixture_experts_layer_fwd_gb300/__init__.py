@@ -10,7 +10,7 @@ call does, and fails loudly if the library has not been built.
 from .api import (MOE_EPI_STORE_BF16, MOE_EPI_SWIGLU_BF16, MOE_EPI_SWIGLU_MX, MOE_EPI_SWIGLU_NVFP4, MOE_FMT_BF16,
                   MOE_FMT_MXFP4, MOE_FMT_MXFP8, MOE_FMT_NVFP4, ForwardGraph, moe_combine, moe_forward,
                   moe_forward_host, moe_forward_host_pipelined, moe_forward_profiled, moe_forward_workspace_size, moe_grouped_gemm,
-                  moe_kv4_attention, moe_kv_compact, moe_kv_copy_pages, moe_kv_extend, moe_kv_fork, moe_kv_free,
+                  moe_kv4_attention, moe_kv_compact, moe_kv_copy_pages, moe_kv_extend, moe_kv_extend_ex, moe_kv_fork, moe_kv_free,
                   moe_permute, moe_permute_noalloc, moe_qk_norm_rope, moe_quant_mx, moe_quant_nvfp4, moe_route, moe_route_permute,
                   moe_selftest_attention_wait_timeout, moe_selftest_grid_barrier_timeout, moe_selftest_wait_timeout, moe_set_wait_timeout_ns,
                   moe_shared_gate, moe_sync_status, moe_version)
@@ -22,5 +22,5 @@ __all__ = ["MOE_EPI_STORE_BF16", "MOE_EPI_SWIGLU_BF16", "MOE_EPI_SWIGLU_MX", "MO
            "ForwardGraph", "moe_combine", "moe_forward", "moe_forward_host", "moe_forward_host_pipelined", "moe_forward_profiled",
            "moe_forward_workspace_size", "moe_grouped_gemm", "moe_permute", "moe_permute_noalloc", "moe_quant_nvfp4",
            "moe_route", "moe_route_permute", "moe_selftest_attention_wait_timeout", "moe_selftest_grid_barrier_timeout", "moe_selftest_wait_timeout", "moe_set_wait_timeout_ns", "moe_shared_gate", "moe_sync_status",
-           "moe_qk_norm_rope", "moe_kv4_attention", "moe_kv_extend", "moe_kv_fork", "moe_kv_free", "moe_kv_compact",
+           "moe_qk_norm_rope", "moe_kv4_attention", "moe_kv_extend", "moe_kv_extend_ex", "moe_kv_fork", "moe_kv_free", "moe_kv_compact",
            "moe_kv_copy_pages", "moe_version", "KV4Cache", "MoELayer", "NVFP4Tensor", "quantize_weights"]

@@ -758,14 +758,27 @@ def _like(out, name, t, inplace, stream):
 
 
 def moe_kv_extend(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
-                  page_size: int, inplace: bool = False, out: Optional[dict] = None,
-                  kv_lens: Optional[torch.Tensor] = None, stream=None) -> dict:
+                  page_size: int, inplace: bool = False, out: Optional[dict] = None, stream=None) -> dict:
     """Room for new tokens: row r gets tokens q_offsets[r] .. q_offsets[r+1]
     (int32 [rows + 1], T tokens in all).  Returns dict(table, lens, refs,
     slots int64 [T], pos int32 [T]); inplace=True writes the state back into
-    the arguments, `out` may hold any of the outputs.  kv_lens int32 [rows],
-    where given, gets the lengths for this step's attention: 0 for a row that
-    found no room."""
+    the arguments, `out` may hold any of the outputs."""
+    return _kv_extend(q_offsets, T, table, lens, refs, page_size, inplace, out, None, stream)
+
+
+def moe_kv_extend_ex(q_offsets: torch.Tensor, T: int, table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
+                     page_size: int, inplace: bool = False, out: Optional[dict] = None, stream=None) -> dict:
+    """moe_kv_extend, and kv_lens int32 [rows]: the lengths for this step's
+    attention, 0 for a row that found no room (a new tensor, or out's)."""
+    kv_lens = (out or {}).get("kv_lens")
+    if kv_lens is None:
+        kv_lens = torch.empty_like(lens) if stream is None else _empty(lens.shape, lens.dtype, lens.device, stream)
+    r = _kv_extend(q_offsets, T, table, lens, refs, page_size, inplace, out, kv_lens, stream)
+    r["kv_lens"] = kv_lens
+    return r
+
+
+def _kv_extend(q_offsets, T, table, lens, refs, page_size, inplace, out, kv_lens, stream) -> dict:
     S, M, N = _kv_state(table, refs, lens)
     dev = table.device
     try:
@@ -876,7 +889,7 @@ __all__ = ["MOE_FMT_BF16", "MOE_FMT_NVFP4", "MOE_FMT_MXFP8", "MOE_FMT_MXFP4", "m
            "moe_route_permute", "moe_quant_nvfp4", "MOE_EPI_SWIGLU_MX",
            "moe_permute_noalloc", "moe_grouped_gemm", "moe_combine", "moe_shared_gate",
            "moe_forward_workspace_size", "moe_forward", "moe_forward_profiled", "moe_forward_host",
-           "moe_forward_host_pipelined", "moe_qk_norm_rope", "moe_kv4_attention", "moe_kv_extend", "moe_kv_fork",
+           "moe_forward_host_pipelined", "moe_qk_norm_rope", "moe_kv4_attention", "moe_kv_extend", "moe_kv_extend_ex", "moe_kv_fork",
            "moe_kv_free", "moe_kv_compact", "moe_kv_copy_pages",
            "ForwardGraph"]
 

@@ -55,8 +55,8 @@ class KV4Cache:
             raise ValueError(f"counts: expected {rows} numbers of new tokens, one per row, got {list(counts)}")
         offsets = [0, *itertools.accumulate(map(int, counts))]
         q_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
-        r = api.moe_kv_extend(q_offsets, offsets[-1], self.table, self.lens, self.refs, self.page_size, inplace=True,
-                              kv_lens=self.kv_lens)
+        r = api.moe_kv_extend_ex(q_offsets, offsets[-1], self.table, self.lens, self.refs, self.page_size, inplace=True,
+                                 out=dict(kv_lens=self.kv_lens))
         self.q_offsets, self.slots, self.pos = q_offsets, r["slots"], r["pos"]
 
     def attend(self, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,

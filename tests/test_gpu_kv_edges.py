@@ -364,13 +364,14 @@ def test_lengths_of_a_step_are_checked():
     table, lens, refs = i(3, 2) - 1, i(3), i(8)
     for bad in (i(4), i(3).long(), torch.zeros(3, dtype=I32)):
         with pytest.raises((TypeError, ValueError), match="kv_lens"):
-            m.moe_kv_extend(i(4), 0, table, lens, refs, 32, kv_lens=bad)
+            m.moe_kv_extend_ex(i(4), 0, table, lens, refs, 32, out=dict(kv_lens=bad))
     with pytest.raises(ValueError, match="q_offsets"):
-        m.moe_kv_extend([0, 0, 0, 0], 0, table, lens, refs, 32)
+        m.moe_kv_extend_ex([0, 0, 0, 0], 0, table, lens, refs, 32)
     with pytest.raises(m._lib.MoEError):
-        m.moe_kv_extend(i(4), 0, table, lens, refs, 32, inplace=True, kv_lens=lens)
+        m.moe_kv_extend_ex(i(4), 0, table, lens, refs, 32, inplace=True, out=dict(kv_lens=lens))
     kv = i(3) + 9
-    o = m.moe_kv_extend(dev([0, 3, 3, 90], I32), 90, table, lens, refs, 32, kv_lens=kv)  # the third has no room
+    o = m.moe_kv_extend_ex(dev([0, 3, 3, 90], I32), 90, table, lens, refs, 32, out=dict(kv_lens=kv))  # the third has no room
+    assert o["kv_lens"] is kv
     assert m.moe_sync_status() == 1 and kv.tolist() == [3, 0, 0] and o["lens"].tolist() == [3, 0, 0]
 
 
