@@ -545,7 +545,15 @@ int moe_qk_norm_rope(const uint16_t* q, long long q_stride, const uint16_t* k, l
  * with q_stride elements between tokens, out bf16 [T][Hq][D].  Rows of no
  * sequence are not written.  Offsets that fall, lengths past the table and
  * pages outside the pool are clamped (the last are reported).  The result of
- * a call is the same each time, whatever the order its blocks ran in. */
+ * a call is the same each time, whatever the order its blocks ran in.
+ * Numbers: cache values without their global scale are exact in fp16, and so
+ * are queries, each row times a power of two, down to 2^-29 of the row's
+ * largest value (rounded to fp16's spacing below that).  Scores, sums and
+ * outputs are held in fp32.  Weights are exponentials by the hardware's
+ * approximation (2 ulp of fp32); they are summed as they are and rounded to
+ * fp16 (2^-12 of each, at most 2^-32 of the row's largest) where they meet
+ * the values.  The output is rounded once more, to bf16 (2^-9), which is most
+ * of its error. */
 size_t moe_kv4_attention_workspace_size(int T, int B, int Hq, int Hkv, int D);
 int moe_kv4_attention(const uint16_t* q, long long q_stride, int T, int Hq,
                       const uint8_t* pool, int num_pages, int page_size, int Hkv, int D,

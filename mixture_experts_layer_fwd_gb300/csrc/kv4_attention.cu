@@ -20,7 +20,7 @@
 // row's largest; P is rounded to fp16 (2^-12); all sums are fp32.  The
 // global scales and Q's power of two go into the softmax scale and the output.
 //
-// 64 sequences of 8192 keys, 64 heads on 4 of 64: 68 us (2.3 TB/s); the matrix
+// 64 sequences of 8192 keys, 64 heads on 4 of 64: 67 us (2.3 TB/s); the matrix
 // instructions and the conversions share issue slots (11.5 cycles per product
 // with its two conversions and two multiplications, and scheduler).  Heads of
 // 128 took 198 us this way where kv4_decode.cu takes 175; three groups of four
@@ -603,9 +603,13 @@ Layout layout(AttnParams& p, int D, void* ws) {
   Layout r;
   // Rows per sequence and kv head on average: the 16-row kernels expand the
   // cache's codes again for every 16 rows, the 256-row kernel once, at the price
-  // of products 256 rows wide.  64 sequences of 8192 keys, 4 kv heads of 128, 16 /
-  // 32 / 48 / 64 rows: 85 / 151 / 217 / 282 us against 239 / 241 / 241 / 242;
-  // of 64: 68 / 112 / 160 / 203 against 176 / 176 / 177 / 177.
+  // of products 256 rows wide.  64 sequences of 8192 keys, 4 kv heads of 128: 85 /
+  // 151 / 215 us for 16 / 32 / 48 rows on the one, 223 for 64 on the other, which
+  // takes about as long for fewer (242 / 241 / 241 / 239 when it was measured for
+  // 64 .. 16, and the one 282 for 64); heads of 64: 67 / 109 / 156, and 170 (203).
+  // The rule takes the whole call's average, so a batch of single tokens beside a
+  // chunk runs on one of the two: 255 single tokens and a chunk of 512, 4096 keys
+  // each, 401 us, where two calls take 152 and 83.
   const bool tiles16 = static_cast<long long>(p.T) * p.G <= 48ll * p.B;
   r.rows = tiles16 ? kRows : kTileRows;
   r.blocks = tiles16 && D != 128 ? kGroups * num_sms() : num_sms();

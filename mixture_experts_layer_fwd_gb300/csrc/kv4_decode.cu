@@ -6,7 +6,8 @@
 //   O^T [128 d][16 rows]   += V^T P^T      A = V from shared memory, B = P
 //
 // so that 16 rows cost a 16-wide product and not a 128-wide one (measured: 49
-// cycles for 16 keys of either product, 65 with the rows on the M side).
+// cycles for 16 keys of either product, 47 where the two alternate, 65 with the
+// rows on the M side).
 // V lies in shared memory key by key as it comes from the codes, rows (d)
 // contiguous, so neither operand is transposed on the way; the order of d in K
 // and Q is free, so a lane of an expanding warp takes 16 consecutive bytes.
@@ -28,13 +29,17 @@
 // a group's 128 threads reduce over the keys, and O is rescaled.  Numbers are
 // as in the 16-row kernel on mma instructions.
 //
-// Bound: the cache's bytes, 18 KB per tile, 0.41 us of an SM's share of HBM.
-// The two products take 0.40 us of the tensor pipe, expanding about as much of
-// the issue slots; what is left on top is the instruction cache (eight
-// programs of 75 KB together run side by side: loops unrolled further, or code
-// at an item's end in the warps that everything waits for, cost more than they
-// save) and the hand-over between roles, 0.57 us per tile in all: 256 sequences of
-// up to 8192 keys, 64 heads on 4, 175 us (3.7 TB/s, 0.55 of a copy).
+// Bound: three things come close to each other, of 0.57 us (1090 cycles) per tile.
+// The cache's bytes, 18 KB, are 0.41 us of an SM's share of HBM.  The two
+// products are 0.39 us: 16 instructions that hold the tensor pipe for 47 cycles
+// each, whichever of the two they belong to and into however many accumulators
+// (measured alone; the multiplication in one takes 8 of the 47, which is all
+// that the pipe's counter shows, 10 %).  Expanding and the softmax take 70 % of
+// the issue slots.  On top come the hand-over between roles and the instruction
+// cache (eight programs of 75 KB together run side by side: loops unrolled
+// further, or code at an item's end in the warps that everything waits for, cost
+// more than they save): 256 sequences of up to 8192 keys, 64 heads on 4, 175 us
+// (3.7 TB/s, 0.55 of a copy).
 #include "kv4_attention.cuh"
 
 namespace moe {

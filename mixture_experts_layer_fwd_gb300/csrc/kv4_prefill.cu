@@ -24,8 +24,8 @@
 // Numbers are as in the 16-row kernel: codes times block scales and Q times a
 // power of two are exact in fp16, P is rounded to fp16, sums are fp32.
 //
-// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.97 ms, 1.42 PFLOP/s; the
-// same with heads of 64 0.88 ms.  What bounds it is the chain scores, softmax,
+// 4096 queries on 12289 keys, 64 heads on 4 of 128: 0.96 ms, 1.43 PFLOP/s; the
+// same with heads of 64 0.83 ms.  What bounds it is the chain scores, softmax,
 // weights, next scores of a tile, since scores and weights share columns.  Half
 // a row per thread 1.17 against 1.21 ms, one tester of a barrier for the eight
 // warps of a tile 1.09 against 1.13, walking the items in a warp of its own
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tiles_kernel(const AttnParam
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t ts = tmem + lanes + g * 128 + 64 * h, to = tmem + lanes + 256 + g * 128 + h * (D / 2);
       // One warp of the tile's eight tests a barrier, the others wait for it at a
-      // hardware barrier: eight warps testing took half the issue slots.
+      // hardware barrier (1.09 ms; all eight testing 1.13).
       const int tile_bar = 9 + g;
       const bool tests = (warp & 7) == 0;
       float* const give = &bars.swap[g][h][r];
