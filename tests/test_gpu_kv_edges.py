@@ -44,6 +44,8 @@ def test_attention_waits_give_up_near_their_limit(lazy, limit_us):
     """They count tests of about 4 us (5 % more where they sleep in between): within a factor of two of the limit."""
     m = moe()
     t = [torch.cuda.Event(enable_timing=True) for _ in range(2)]
+    m.moe_selftest_attention_wait_timeout(1000, lazy)  # the first launch loads the kernel
+    assert m.moe_sync_status() == 5
     t[0].record()
     m.moe_selftest_attention_wait_timeout(1000 * limit_us, lazy)
     t[1].record()
