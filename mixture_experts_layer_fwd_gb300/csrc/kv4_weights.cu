@@ -643,6 +643,11 @@ DEVINL void many_rows(const Params& p, Stage<D>& sh) {
 //   11        takes items (sequence, kv head, keys) and publishes them, one ahead
 //   12-15     expand the next item's keys into the swizzle that the instructions read
 //
+// Which tile is whose goes by the count of tiles over all items, not by the place in an
+// item: a slot of the rings of tiles and of columns then has the same reader for good, who
+// waits for each of its uses.  (A reader that left one out could find the barrier in the
+// phase before, which has the parity that it waits for, and read what has not come.)
+//
 // Bound: a tile of 128 x 128 scores takes its products 710 cycles and its four warps 990
 // (the exponentials; two fours, so 500); items end and begin.  256 keys to an item,
 // which halves the rows' way from L2, was slower (1169 against 878 us on the long chunk).
@@ -655,6 +660,7 @@ struct TileCfg {
   static constexpr int SUB = 128 * 128;             // 64 values of 128 keys or rows
   static constexpr int TILE = 128 * D * 2;          // of keys or rows
   static constexpr int STAGES = D == 128 ? 4 : 8;   // tiles of rows in flight
+  static_assert(STAGES % 2 == 0 && kColumnSlots % 2 == 0, "a slot has one reader");
   static constexpr int Q0 = 2 * TILE;               // behind two items' keys
   static constexpr int COLUMNS0 = Q0 + STAGES * TILE;
   static constexpr int COLUMNS = 16 * static_cast<int>(sizeof(Columns));
@@ -735,7 +741,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weights_tiles_kernel(const Pa
       if (p.window > 0 && hi > 0)
         hi = static_cast<int>(max(0ll, min(static_cast<long long>(it.nq), static_cast<long long>(key) + p.window - base))) * p.G;
       uint64_t sum[2] = {0, 0};
-      for (int f = grp; f < it.n; f += 2, ++uses) {
+      for (int f = static_cast<int>((stage0 + grp) & 1); f < it.n; f += 2, ++uses) {
         const int buf = 2 * grp + (uses & 1), r0 = (it.q0 + f) * 128;
         const uint32_t stage = stage0 + f, slot = stage % kColumnSlots;
         const Columns* c = reinterpret_cast<const Columns*>(smem + C::COLUMNS0 + slot * C::COLUMNS);
@@ -852,7 +858,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weights_tiles_kernel(const Pa
     const uint64_t dk = smem_desc_kmajor_sw128(sk), dq = smem_desc_kmajor_sw128(sk + C::Q0);
     ItemReader items;
     uint32_t turn = 0, uses = 0;
-    int st = 0;
+    int st = 0;  // its parity is that of the count of tiles
     bool gone = false;
     for (uint32_t i = 0; !gone; ++i) {
       const Item it = items.next(bars.items, polls, p.err, abort);
@@ -860,7 +866,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) weights_tiles_kernel(const Pa
       const int kb = i & 1;
       wait_warp(&bars.kfull[kb], i >> 1 & 1, polls, p.err, abort);
       for (int f = 0; f < it.n && !gone; ++f) {
-        if ((f & 1) == grp) {
+        if ((st & 1) == grp) {
           const int buf = 2 * grp + (uses & 1);
           wait_warp(&bars.qfull[st], turn, polls, p.err, abort);
           if (uses >= 2) wait_warp(&bars.sempty[buf], ((uses >> 1) - 1) & 1, polls, p.err, abort);

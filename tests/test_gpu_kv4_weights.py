@@ -118,6 +118,19 @@ def test_weights_of_few_rows_among_many_empty_sequences(D, G):
         check_weights(attn_case(D, Hkv, G, 64, qs, kvs, seed=B), 64, D ** -0.5, window=0 if B != 33 else 50)
 
 
+@pytest.mark.parametrize("D,Hkv,G,qs,kvs", [(128, 4, 3, [120, 125], [4800, 5200]),   # 3 tiles of 128 rows to an item
+                                            (128, 4, 2, [190, 65], [3000, 7000]),    # 3; 2
+                                            (64, 4, 3, [120, 210], [6000, 3000])])   # 3; 5
+def test_weights_of_items_with_an_odd_number_of_tiles(D, Hkv, G, qs, kvs):
+    """Several items to a block: a slot of the rings holds tiles of either place in an item."""
+    c, scale = attn_case(D, Hkv, G, 64, qs, kvs, seed=D + G), D ** -0.5
+    lse = reference_lse(c, 64, scale, True, 0)
+    want = check_weights(c, 64, scale, lse=lse, more=0)
+    before = dev(np.random.default_rng(0).exponential(size=tuple(want.shape)).astype(F32))  # as check_weights' own
+    for _ in range(20):
+        assert torch.equal(call(c, 64, lse, before.clone(), scale), want)
+
+
 @pytest.mark.parametrize("D,causal,window", [(128, True, 0), (64, False, 0), (64, True, 130)])
 def test_weights_of_long_chunks_on_few_keys(D, causal, window):
     """Few items of many rows: their rows are split, the sums join."""
