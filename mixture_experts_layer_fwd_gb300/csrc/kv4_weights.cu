@@ -847,11 +847,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) weights_tiles_kernel(const Pa
         if (++st == C::STAGES) st = 0, turn ^= 1;
       }
     }
-    // no block ends with bytes on their way to its shared memory
-    for (uint32_t u = uses > C::STAGES ? uses - C::STAGES : 0; u < uses; ++u) {
+    // no block ends with bytes on their way to its shared memory: the last uses of all slots
+    // (an older tile's columns may be on their way still where the sums were given up)
+    for (uint32_t u = uses > C::STAGES ? uses - C::STAGES : 0; u < uses; ++u)
       mbar_wait_warp(&bars.qfull[u % C::STAGES], (u / C::STAGES) & 1, kLandNs, p.err, nullptr);
+    for (uint32_t u = uses > kColumnSlots ? uses - kColumnSlots : 0; u < uses; ++u)
       mbar_wait_warp(&bars.cfull[u % kColumnSlots], (u / kColumnSlots) & 1, kLandNs, p.err, nullptr);
-    }
   } else if (warp < kWalk) {
     // ======================================================= matrix instructions
     const int grp = warp - kIssue;
