@@ -21,7 +21,7 @@
 // flight.
 //
 // On the GPU alone (matrices in turn, none in L2): 1 token 1024 x 4096 6.0 us, 5 tokens
-// 9216 x 4096 11.5 us, 16 tokens 4096 x 8192 17 us, 1 / 8 / 24 / 32 tokens 151936 x 4096
+// 9216 x 4096 11.0 us, 16 tokens 4096 x 8192 16 us, 1 / 8 / 24 / 32 tokens 151936 x 4096
 // 62 / 66 / 100 / 121 us (5.6 / 5.3 / 3.5 / 2.9 TB/s).  Registers instead of rings 78 /
 // 82 / 132 / 134 us there, 7.1 against 6.7 us for 1 token 4096 x 4096.
 #include <cmath>
@@ -131,43 +131,42 @@ __global__ void __launch_bounds__(kPrepThreads) linear_prepare_kernel(const Para
 
 // Few tokens: a block brings them into place itself, a launch less (with the call, 1 token
 // 1024 x 4096 14 against 19 us, 16 tokens 4096 x 8192 18.6 against 19.8, although the GPU
-// alone takes 2 us more there: every block reads all tokens).  A token's largest
-// value mostly lies between 2^-4 and 2^7, where 2^8 times the token is as exact as its own
-// power of two would make it, to 2^-29 of that value; so the tokens are read once, and
-// those for which it is not so once more.
-constexpr int kInline = 16, kInlineK = 16384, kUsual = 8;
+// alone takes 1 us more there: every block reads all tokens).  They are read once: bf16
+// as it lies goes to its place, and when the largest value of each token is known (of the
+// values that the block has) a thread brings its own units to fp16 there.
+constexpr int kInline = 16, kInlineK = 16384;
 template <bool MAP>
-DEVINL void stage(const Params& p, uint4* xs, uint32_t* s_top, int k0, int n, int t0, int t1, int e) {
-  const int units = n * Cfg<MAP>::kUnits, total = units * (t1 - t0);
-  const float up = power_of_two(e);
+DEVINL void stage(const Params& p, uint4* xs, int* s_exp, uint32_t* s_top, int k0, int n) {
+  const int units = n * Cfg<MAP>::kUnits, total = units * p.T;
+  constexpr int kLanes = Cfg<MAP>::kUnits;  // side by side that have the same token (a multiple of these is all there is)
+  static_assert(kLanes == 16 || kLanes == 32, "half of a warp, or one");
+  const int lane = threadIdx.x & 31;
+  const uint32_t same = kLanes == 32 ? 0xFFFFFFFFu : 0xFFFFu << (lane & 16);
   constexpr int kBatch = 5;  // loads of a thread in flight
 #pragma unroll 1
   for (int i0 = threadIdx.x; i0 < total; i0 += kBatch * Cfg<MAP>::kThreads) {
     uint4 v[kBatch];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * Cfg<MAP>::kThreads, t = t0 + i / units, k = k0 * Cfg<MAP>::kStep + 8 * (i % units);
+      const int i = i0 + b * Cfg<MAP>::kThreads, t = i / units, k = k0 * Cfg<MAP>::kStep + 8 * (i % units);
       v[b] = i < total && k < p.K ? __ldg(reinterpret_cast<const uint4*>(p.x + t * p.x_stride + k)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const int i = i0 + b * Cfg<MAP>::kThreads, t = t0 + i / units;
+      const int i = i0 + b * Cfg<MAP>::kThreads, t = i / units;
       if (i >= total) break;
-      xs[t * token_units<MAP>(p.slab) + unit_at<MAP>(i % units)] = bf16x8_to_f16x8(v[b], up);
-      atomicMax(s_top + t, bf16x8_top(v[b]));
+      xs[t * token_units<MAP>(p.slab) + unit_at<MAP>(i % units)] = v[b];
+      const uint32_t top = __reduce_max_sync(same, bf16x8_top(v[b]));
+      if (lane % kLanes == 0) atomicMax(s_top + t, top);
     }
   }
-}
-template <bool MAP>
-DEVINL void stage_all(const Params& p, uint4* xs, int* s_exp, uint32_t* s_top, int k0, int n) {
-  stage<MAP>(p, xs, s_top, k0, n, 0, p.T, kUsual);
   __syncthreads();
-  for (int t = 0; t < p.T; ++t) {
-    const uint32_t top = s_top[t];
-    const int e = static_cast<int>(top >> 7) - 127;  // 2^e <= the largest value < 2^(e + 1)
-    const bool usual = e >= -4 && e < 7;
-    if (threadIdx.x == 0) s_exp[t] = usual ? kUsual : f16_exponent(top);
-    if (!usual) stage<MAP>(p, xs, s_top, k0, n, t, t + 1, f16_exponent(top));
+  if (static_cast<int>(threadIdx.x) < p.T) s_exp[threadIdx.x] = f16_exponent(s_top[threadIdx.x]);
+#pragma unroll 1
+  for (int i = threadIdx.x; i < total; i += Cfg<MAP>::kThreads) {
+    const int t = i / units;
+    uint4& unit = xs[t * token_units<MAP>(p.slab) + unit_at<MAP>(i % units)];
+    unit = bf16x8_to_f16x8(unit, power_of_two(f16_exponent(s_top[t])));
   }
 }
 
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(Cfg<MAP>::kThreads, 1) linear_kernel(const Par
   if (INLINE) {
     if (threadIdx.x < kInline) s_top[threadIdx.x] = 0;
     __syncthreads();
-    stage_all<MAP>(p, xs, s_exp, s_top, k0, steps);
+    stage<MAP>(p, xs, s_exp, s_top, k0, steps);
   } else {
     if (threadIdx.x == 0) {
       for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1), s_copied[i] = 0;

@@ -61,9 +61,10 @@ DEVINL uint32_t bf16x8_top(const uint4& v) {
   const uint32_t t = __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
   return max(t & 0xFFFFu, t >> 16);
 }
-// Exponent e of the power of two that brings a row of that largest magnitude
-// below 2^15: exact in fp16 down to 2^-29 of it, off by 2^-40 of it at most below.
-DEVINL int f16_exponent(uint32_t top) { return min(14 + 127 - static_cast<int>(top >> 7), 120); }
+// Exponent e of the power of two that brings a row of that largest magnitude to 2^15 or
+// more, below 2^16 (65280 at most, which fp16 has): exact in fp16 down to 2^-29 of it, off
+// by 2^-40 of it at most below.  (Rows below 2^-105: exact, times 2^120.)
+DEVINL int f16_exponent(uint32_t top) { return min(15 + 127 - static_cast<int>(top >> 7), 120); }
 DEVINL float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126 <= e <= 127
 
 }  // namespace moe

@@ -98,6 +98,27 @@ def test_linear_keeps_the_range_of_its_types(T, N, K):
     check(out, *expected(*a))
 
 
+@pytest.mark.parametrize("T,N,K", [(1, 100, 512), (4, 70, 2080), (16, 40, 4096), (16, 33, 288), (17, 40, 4096), (32, 33, 288)])
+@pytest.mark.parametrize("top", [-90, -4, 0, 6, 15, 90])
+@pytest.mark.parametrize("deep", [False, True])
+def test_small_values_beside_a_large_one_that_meets_no_weight(T, N, K, top, deep):
+    """However many tokens: exact down to 2^-29 of a token's largest value, off by 2^-40 of it at most below."""
+    rng = np.random.default_rng(T + K + top)
+    x = rng.uniform(1, 2, size=(T, K)) * 2.0 ** (top - rng.integers(*((30, 40) if deep else (20, 30)), size=(T, K)))
+    x = (x * rng.choice([-1, 1], size=x.shape)).astype(np.float32)
+    x[:, :16] = 0
+    x[:, 5] = 2.0 ** top
+    _, codes, sf, g = case(T, N, K)
+    sf[:, 0] = 0
+    x = torch.from_numpy(x).bfloat16()
+    w, xd = nvfp4.dequantize(codes, sf, g), x.double().numpy()
+    y, size = xd @ w.T, np.abs(xd) @ np.abs(w).T  # the large value is in neither
+    off = (K / 16 + 16) * 2.0 ** -22 * size + 2.0 ** -23 * np.abs(y)  # as in expected()
+    if deep:
+        off = off + 2.0 ** (top - 40) * np.abs(w).sum(1)
+    check(moe().moe_linear_nvfp4(*put(x, codes, sf, g), out_dtype=torch.float32), y, off)
+
+
 @pytest.mark.parametrize("T,N,K", [(1, 64, 128), (4, 130, 160), (20, 48, 1024)])
 @pytest.mark.parametrize("f32", [False, True])
 def test_linear_adds_and_takes_strided_rows(T, N, K, f32):
