@@ -172,7 +172,10 @@ DEVINL void add_values(Part& a, const Raw<L> (&raw)[kLoads], int i0, float c) {
   for (int k = 0; k < kLoads; ++k) {
     expand(raw[k], v[k]);
 #pragma unroll
-    for (int e = 0; e < kGroup; ++e) m = fmaxf(m, v[k][e]);
+    for (int e = 0; e < kGroup; ++e) {
+      if (TOP) v[k][e] = value_of(v[k][e]);  // (weights: where some sum is no number, see below)
+      m = fmaxf(m, v[k][e]);
+    }
   }
   if (TOP) {
     if (m > a.m) {

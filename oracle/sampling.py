@@ -13,11 +13,11 @@ def target(logits, temperature: float) -> np.ndarray:
     counts as the largest finite fp32 number."""
     z = np.asarray(logits, np.float64).copy()
     z[np.isnan(z)] = -np.inf
+    z = np.minimum(z, np.finfo(np.float32).max)
     if not temperature > 0:
         p = np.zeros(len(z))
         p[np.argmax(z)] = 1.0  # the first of equal ones
         return p
-    z = np.minimum(z, np.finfo(np.float32).max)
     e = np.exp((z - z.max()) / temperature)
     return e / e.sum()
 

@@ -16,6 +16,13 @@ def test_target_is_the_softmax():
     assert sampling.target([1.0, np.inf, 3e38, np.inf], 1.0).tolist() == [0, 0.5, 0, 0.5]
 
 
+def test_infinity_counts_as_the_largest_finite_number_in_greedy_rows_too():
+    top = float(np.finfo(np.float32).max)
+    assert sampling.target([1.0, top, np.inf], 0.0).tolist() == [0, 1, 0]
+    assert sampling.target([1.0, np.inf, top], 0.0).tolist() == [0, 1, 0]
+    assert sampling.target([np.nan, 3e38, np.inf], 0.0).tolist() == [0, 0, 1]
+
+
 def test_draw_by_hand():
     w = np.array([0.0, 0.25, 0.0, 0.5, 0.25, 0.0])
     assert [sampling.draw(w, u) for u in (0.0, 0.2499, 0.25, 0.7499, 0.75, 0.9999)] == [1, 1, 3, 3, 4, 4]
