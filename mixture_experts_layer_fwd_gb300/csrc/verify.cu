@@ -38,10 +38,11 @@ DEVINL float near_of(float e) { return 0x1p-17f + fabsf(e) * 0x1p-22f; }
 constexpr int kBits = 40;                              // of a weight's fraction
 constexpr float kLowest = -3.4028234663852886e38f;
 
-struct Part {  // of a row: largest logit, its first index, sum of the weights relative to it
+struct Part {  // of a row: largest logit, its first index (greedy rows; else 0), sum of the weights relative to it
   float m, s;
   int idx, pad;
 };
+constexpr int kNone = 0x7FFFFFFF;  // index where no logit is a number
 struct Sums {  // of kSub values: weights; weights and draft probabilities where p > q
   long long all, over, q;
 };
@@ -126,8 +127,9 @@ DEVINL void expand(const Raw<float>& r, float (&v)[kGroup]) {
   v[0] = r.a.x, v[1] = r.a.y, v[2] = r.a.z, v[3] = r.a.w;
   v[4] = r.b.x, v[5] = r.b.y, v[6] = r.b.z, v[7] = r.b.w;
 }
-// not a number, or -infinity: no weight; infinity: as the largest finite number
-DEVINL float value_of(float v) { return fminf(fmaxf(v, kLowest), -kLowest); }
+// not a number, or -infinity: -infinity, no weight (the lowest finite number has one, beside
+// its equals); infinity: as the largest finite number
+DEVINL float value_of(float v) { return fminf(fmaxf(v, -INFINITY), -kLowest); }
 template <class L>
 DEVINL void load_group(const L* row, int i, int V, float (&v)[kGroup]) {
   expand(load_raw(row, i, V), v);
@@ -178,7 +180,7 @@ DEVINL void add_values(Part& a, const Raw<L> (&raw)[kLoads], int i0, float c) {
     }
   }
   if (TOP) {
-    if (m > a.m) {
+    if (m > a.m || a.idx == kNone) {
 #pragma unroll
       for (int k = kLoads - 1; k >= 0; --k)
 #pragma unroll
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 5) verify_rows_kernel(const Params p
   const int seq = max(before - 1, 0);
   const bool top = greedy(p, seq);
   const float c = sharpness(p, seq).hi;
-  Part a{kLowest, 0.0f, 0x7FFFFFFF, 0};
+  Part a{kLowest, 0.0f, kNone, 0};
   for (; i0 < end; i0 += kChunk) {
     Raw<L> now[kLoads];
 #pragma unroll
@@ -238,14 +240,14 @@ __global__ void __launch_bounds__(kThreads, 5) verify_rows_kernel(const Params p
     else add_values<false, L>(a, now, i0, c);
   }
   if (a.s != a.s) {  // some logit is infinite or not a number: once more with what counts for it
-    a.s = 0.0f, a.m = value_of(a.m);
+    a.s = 0.0f, a.m = value_of(a.m);  // (kLowest or more)
     for (i0 = begin; i0 < end; i0 += kThreads * kGroup) {
       float v[kGroup];
       load_group(row, i0, p.V, v);
       for (int e = 0; e < kGroup; ++e) a.s += ex2((v[e] - a.m) * c);
     }
   }
-  if (a.m == kLowest) a.s = 0.0f, a.idx = 0x7FFFFFFF;
+  if (!top && a.s > 0.0f) a.idx = 0;  // the largest one's weight is 1
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) join(a, shuffle(a, x), c);
   if (lane == 0) s_part[warp] = a;
@@ -433,7 +435,7 @@ __global__ void __launch_bounds__(kThreads) verify_token_kernel(const Params p) 
     float l, q, u;
   };
   auto drafted = [&](int t) {
-    Draft d{p.tokens[t + 1], kLowest, 0.0f, p.u[t + 1]};
+    Draft d{p.tokens[t + 1], -INFINITY, 0.0f, p.u[t + 1]};
     if (d.word >= 0 && d.word < p.V) {
       if (sizeof(L) == 2) d.l = __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[t * p.stride + d.word]);
       else d.l = static_cast<const float*>(p.logits)[t * p.stride + d.word];
@@ -452,7 +454,7 @@ __global__ void __launch_bounds__(kThreads) verify_token_kernel(const Params p) 
   for (int i0 = 0; stop < 0; i0 += kWarps) {
     const int i = i0 + warp, t = first + i;
     if (i <= n) {
-      Part a{kLowest, 0.0f, 0x7FFFFFFF, 0};
+      Part a{kLowest, 0.0f, kNone, 0};
       for (int k = lane; k < p.chunks; k += 32) join(a, p.parts[static_cast<long long>(t) * p.chunks + k], x.c_hi);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) join(a, shuffle(a, o), x.c_hi);
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads) verify_token_kernel(const Params p) 
             const float uq = d.u * d.q;
             if (top) {
               flag = d.word == a.idx && uq < 1.0f;
-            } else if (d.l > kLowest) {
+            } else if (d.l > kLowest || (d.l == kLowest && a.m == kLowest)) {  // (a mask, unless all are)
               // (far below 2^-100 p is still no 0)
               const float e = (d.l - a.m) * x.c_hi, pw = ex2(e) / a.s;
               if (uq == 0.0f) flag = 1;
@@ -498,10 +500,10 @@ __global__ void __launch_bounds__(kThreads) verify_token_kernel(const Params p) 
   const int t = first + stop;
   const bool refused = stop < n;
   if (blockIdx.x == 0 && threadIdx.x == 0) p.accepted[b] = stop, p.refused[b] = n - stop;
-  if (top || at.m == kLowest) {  // no logit that is a number: no token
+  if (top || at.idx == kNone) {  // no logit that is a number: no token
     if (blockIdx.x == 0 && threadIdx.x == 0) {
-      p.token[b] = at.m == kLowest ? -1 : at.idx;
-      if (at.m == kLowest) atomicOr(p.err, kErrBadIndex);
+      p.token[b] = at.idx == kNone ? -1 : at.idx;
+      if (at.idx == kNone) atomicOr(p.err, kErrBadIndex);
     }
     return;
   }
@@ -612,7 +614,7 @@ __global__ void __launch_bounds__(kThreads) verify_token_kernel(const Params p) 
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const bool have = i + e >= 0 && i + e < p.V;
-    v[e] = !have ? kLowest : value_of(sizeof(L) == 2 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[i + e])
+    v[e] = !have ? -INFINITY : value_of(sizeof(L) == 2 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(row)[i + e])
                                                      : reinterpret_cast<const float*>(row)[i + e]);
     q[e] = have && !plain && probs ? prob_of(probs[i + e]) : 0.0f;
   }
