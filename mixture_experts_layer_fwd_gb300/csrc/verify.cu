@@ -10,7 +10,7 @@
 // 2^(log2(p) - log2(largest p)) are integers, multiples of 2^-40, formed by fp32
 // pairs within 2^-26 of their value, and their sums are exact.  Bound: the logits,
 // read once by the first launch, which makes fast fp32 sums of every row (within
-// 2^-18), enough to decide on a drafted token unless u q(x) is that near to p(x);
+// 2^-16 for 151936 words), enough to decide on a drafted token unless u q(x) is that near to p(x);
 // the row in question is then summed in integers.  The second launch reads the one
 // row per sequence that the next token comes from, and its draft probabilities;
 // the last of a sequence's blocks finds the token.
@@ -31,10 +31,12 @@ constexpr int kLoads = 2;                              // groups of a lane in fl
 constexpr int kChunk = kThreads * kGroup * kLoads;     // values of a row that a block of the first launch takes at a time
 constexpr int kSub = 2 * 32 * kGroup;                  // whose sums the second launch writes down
 static_assert(kSub == 2 * kThreads, "two values per thread");
-// What the fast p(x) may be off, relative to it: three roundings of an exponent e of up
-// to |e| 2^-25 each and one of the exponential of 2^-22 in p(x) itself; in the sum of
-// up to 2^22 weights those of weights that matter (|e| <= 22), and 2^-20 of the sums.
-DEVINL float near_of(float e) { return 0x1p-17f + fabsf(e) * 0x1p-22f; }
+// What the fast p(x) may be off at most, relative to it.  An exponent e: its three roundings,
+// |e| 2^-22.9 of the weight; in the sum of up to 2^22 weights, the largest of them 1, 2^-18.8
+// (17 |e| on average of the weight at most).  With 2^-22 per exponential, nine additions of
+// a lane's chunk, the quotient and u q: kNear.  Each further step of a sum, a lane's next
+// chunk or a join, rounds an exponential, a product and a sum: kNearStep.
+constexpr float kNear = 0x1p-18f, kNearStep = 0x1.8p-22f, kNearExponent = 0x1p-22f;
 constexpr int kBits = 40;                              // of a weight's fraction
 constexpr float kLowest = -3.4028234663852886e38f;
 
@@ -58,6 +60,7 @@ struct Params {
   int T, V, B;
   int chunks, chunk;    // blocks of a row in the first launch, values of each
   int subs, per_warp;
+  float near;           // how far the fast p(x) may be off, its own exponent aside
   Part* parts;    // [T][chunks]
   Sums* sums;     // [B][subs]
   unsigned* done; // [B] blocks of the second launch that have written theirs
@@ -473,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) verify_token_kernel(const Params p) 
               const float e = (d.l - a.m) * x.c_hi, pw = ex2(e) / a.s;
               if (uq == 0.0f) flag = 1;
               else if (e < -100.0f) flag = uq < 0x1p-80f ? 2 : 0;
-              else flag = fabsf(uq - pw) <= near_of(e) * pw ? 2 : uq < pw;
+              else flag = fabsf(uq - pw) <= (p.near + fabsf(e) * kNearExponent) * pw ? 2 : uq < pw;
             }
           }
         }
@@ -699,6 +702,8 @@ extern "C" int moe_verify_draft(const void* logits, int logits_f32, long long lo
   const int most = chunks_of(V), split = std::max(1, std::min(most, num_sms() * 5 / T));
   p.chunk = (most + split - 1) / split * kChunk;
   p.chunks = (most * kChunk + p.chunk - 1) / p.chunk;
+  // a lane's chunks, joins of a warp's lanes, of warps, of a row's chunks by a lane, of those lanes
+  p.near = kNear + (p.chunk / kChunk + 5 + kWarps + (p.chunks + 31) / 32 + 5) * kNearStep;
   // a warp takes several parts of a row where there are more than a few rounds of them
   // (1 / 2 / 4 / 8: 24 / 28 / 32 / 42 us for one sequence, 69 / 67 / 71 / 95 for 64)
   p.per_warp = static_cast<int>(
