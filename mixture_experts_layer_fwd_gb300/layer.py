@@ -26,17 +26,26 @@ class NVFP4Tensor:
     def linear(self, x: torch.Tensor, add: Optional[torch.Tensor] = None,
                out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
         """x bf16 [T, cols] times this matrix [rows, cols] (one group), plus add bf16
-        [T, rows]: moe_linear_nvfp4 for up to 32 tokens; more go through
-        moe_grouped_gemm as one group (rows % 32 == 0, cols % 64 == 0, a product
-        rounded to bf16 before the sum)."""
+        [T, rows]: moe_linear_nvfp4 for up to 32 tokens.  More go through
+        moe_grouped_gemm as one group (the product is then rounded to bf16 before
+        the sum), and 32 at a time through moe_linear_nvfp4 where fp32 is asked for
+        or the matrix is none of moe_grouped_gemm's (rows % 32, cols % 64)."""
         N, K = self.codes.shape[-2], self.codes.shape[-1] * 2
         codes, sf = self.codes.view(N, K // 2), self.sf.view(N, K // 16)
         T = x.shape[0]
         if T <= 32:
             return api.moe_linear_nvfp4(x, codes, sf, self.g, add=add, out_dtype=out_dtype)
+        x = x.contiguous()
+        if out_dtype == torch.float32 or N % 32 or K % 64:
+            if add is not None and add.shape != (T, N):
+                raise ValueError(f"add: expected [{T}, {N}], got {tuple(add.shape)}")
+            out = torch.empty(T, N, dtype=out_dtype, device=x.device)
+            for t in range(0, T, 32):
+                api.moe_linear_nvfp4(x[t:t + 32], codes, sf, self.g, add=None if add is None else add[t:t + 32],
+                                     out_dtype=out_dtype, out=out[t:t + 32])
+            return out
         group = torch.arange(0, T + 1, T, dtype=torch.int32, device=x.device)
-        y = api.moe_grouped_gemm(MOE_FMT_BF16, MOE_FMT_NVFP4, MOE_EPI_STORE_BF16, group, N, K, x.contiguous(), codes, W_sf=sf,
-                                 W_g=self.g)
+        y = api.moe_grouped_gemm(MOE_FMT_BF16, MOE_FMT_NVFP4, MOE_EPI_STORE_BF16, group, N, K, x, codes, W_sf=sf, W_g=self.g)
         return (y if add is None else y + add).to(out_dtype)
 
 

@@ -237,6 +237,34 @@ def test_a_quantised_matrix_takes_any_number_of_tokens(T):
     assert w.linear(x, out_dtype=torch.float32).dtype == torch.float32
 
 
+@pytest.mark.parametrize("rows,cols", [(96, 256), (50, 96), (40, 320)])
+def test_a_quantised_matrix_gives_fp32_sums_for_any_number_of_tokens(rows, cols):
+    """What is asked for in fp32 is not rounded to bf16 on the way, whatever the matrix's size:
+    a token's outputs are those that it has alone among up to 32."""
+    import mixture_experts_layer_fwd_gb300 as m
+    from oracle import nvfp4
+    g = torch.Generator("cuda").manual_seed(rows)
+    w = m.quantize_weights((torch.randn(rows, cols, generator=g, device="cuda") / 16).bfloat16())
+    wd = nvfp4.dequantize(w.codes.cpu().numpy(), w.sf.cpu().numpy(), w.g.cpu().numpy()[0])
+    x, add = (torch.randn(77, n, generator=g, device="cuda").bfloat16() for n in (cols, rows))
+    y, size = to_np_f32(x).astype(np.float64) @ wd.T, np.abs(to_np_f32(x)) @ np.abs(wd).T
+    for T in (32, 33, 64, 77):
+        for a in (None, add[:T]):
+            got = w.linear(x[:T], add=a, out_dtype=torch.float32)
+            want = y[:T] + (0 if a is None else to_np_f32(a))
+            # cols / 16 instructions and 16 parts, 2^-22 of the sum of magnitudes each; the one rounding
+            off = (cols / 16 + 16) * 2.0 ** -22 * size[:T] + 2.0 ** -23 * np.abs(want)
+            assert got.dtype == torch.float32 and got.shape == (T, rows)
+            assert (np.abs(to_np_f32(got) - want) <= off).all()
+            assert w.linear(x[:T], add=a).dtype == torch.bfloat16
+    wide = torch.zeros(40, cols + 8, dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:] = x[:40]
+    assert torch.equal(w.linear(wide[:, 8:], out_dtype=torch.float32), w.linear(x[:40], out_dtype=torch.float32))
+    for bad in (add[:50], add):
+        with pytest.raises(ValueError):
+            w.linear(x[:64], add=bad, out_dtype=torch.float32)
+
+
 def test_speculative_decoding_example_runs():
     r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "speculative_decoding.py")], capture_output=True, text=True,
                        timeout=300)
