@@ -194,10 +194,16 @@ DEVINL void prepare(const Params& p, int block, int blocks, int* s_sum) {
     uint32_t top = 0;
     const long long token = s_start[b] + tok;
     const int head = h * p.G + r - tok * p.G;
+    const float l = have ? p.lse[token * p.Hq + head] : -INFINITY;
+    const bool gives = l != -INFINITY;  // a row without weight is one of zeros, whatever lies in it
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       v[j] = make_uint4(0, 0, 0, 0);
       if (have) v[j] = __ldg(reinterpret_cast<const uint4*>(p.q + token * p.q_stride + head * D + c4 * (D / 4)) + j);
+    }
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+      if (!gives) v[j] = make_uint4(0, 0, 0, 0);
       top = max(top, bf16x8_top(v[j]));
     }
     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -216,11 +222,12 @@ DEVINL void prepare(const Params& p, int block, int blocks, int* s_sum) {
     if (c4 == 0) {
       float2 w = make_float2(0.0f, INFINITY);
       int2 see = make_int2(0, 0);
-      if (have) {
-        const float l = p.lse[token * p.Hq + head];
-        const int place = len - n + tok;
+      if (gives) {
         w.x = p.scale * __ldg(p.g_k + h) * kLog2e * power_of_two(-e);
-        w.y = l == -INFINITY ? INFINITY : l * kLog2e;
+        w.y = l * kLog2e;
+      }
+      if (have) {
+        const int place = len - n + tok;
         see.x = p.window > 0 ? max(place - p.window + 1, 0) : 0;
         see.y = p.causal ? min(max(place + 1, 0), len) : len;
       }

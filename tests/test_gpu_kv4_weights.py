@@ -157,6 +157,19 @@ def test_a_row_with_lse_of_no_keys_gives_nothing_and_nan_goes_where_it_looks():
     assert s[0, :39].isnan().all() and s[0, 39:].isfinite().all() and s[1].isfinite().all()
 
 
+@pytest.mark.parametrize("qs,kvs", [([3, 1], [300, 50]), ([20, 1], [300, 50]), ([150, 1], [300, 50])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_row_with_lse_of_no_keys_gives_nothing_whatever_lies_in_it(D, qs, kvs):
+    """Registers, staged rows and tcgen05: a query of NaN or infinity there is as good as zeros."""
+    c = attn_case(D, 1, 2, 32, qs, kvs, seed=D + qs[0])
+    lse = reference_lse(c, 32, 0.1, True, 0)
+    lse[qs[0] - 1], lse[1, 1], lse[qs[0], 0] = -np.inf, -np.inf, -np.inf
+    q = c["q"].clone()
+    want = check_weights(c, 32, 0.1, lse=lse)
+    q[qs[0] - 1, 0, 5], q[qs[0] - 1, 1], q[1, 1, ::3], q[qs[0], 0] = float("nan"), float("inf"), -float("inf"), float("nan")
+    assert torch.equal(check_weights(c, 32, 0.1, lse=lse, q=q.to(DEV)), want)
+
+
 def test_weights_and_attention_together():
     """With the attention's own lse a query head's weights add up to one."""
     m = moe()
