@@ -626,6 +626,9 @@ int moe_kv4_attention(const uint16_t* q, long long q_stride, int T, int Hq,
  *           the step wrote (the last n of a sequence with n queries) score = w,
  *           for those before them score += w; no other entry is touched.  So a
  *           sequence's sums are right if every one of its steps makes this call.
+ *           Every query counts, those of drafted tokens that are refused later too:
+ *           a step of drafts makes the call when they have been verified, before
+ *           moe_kv_drop, with lse -inf for the refused ones.
  * A row with lse -inf gives no weight.  A row that is not a number gives NaN to
  * each key that it sees.  Sums are fp32, each key's in the order of the rows: the
  * result of a call is the same each time.  Numbers as for moe_kv4_attention.

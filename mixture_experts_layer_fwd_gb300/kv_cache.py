@@ -8,10 +8,11 @@ on the current stream, without a host read.  extend, fork and free take their
 numbers from the host, so a CUDA graph holds attend() calls or the library's calls
 on index tensors, not those three.
 
-A cache may be kept short: with track=True attend() sums up the attention
-weights that each key gets (moe_kv4_weights), and evict() lets the keys with
-the least of them go.  verify() checks a step's drafted tokens and takes the
-refused ones out again.
+A cache may be kept short: with track=True the attention weights that each key
+gets are summed up (moe_kv4_weights), and evict() lets the keys with the least of
+them go.  verify() checks a step's drafted tokens and takes the refused ones out
+again.  What their queries looked at does not count: a step's sums wait for the
+call that ends it.
 """
 from __future__ import annotations
 
@@ -44,7 +45,9 @@ class KV4Cache:
         self.kv_lens = torch.zeros_like(self.lens)  # as the step's attention takes them
         self.refs = torch.zeros(num_pages, dtype=torch.int32, device=dev)
         # what attention gave to each token of each row, and the tokens that evict() has taken from a row
-        self.scores = torch.zeros(layers, rows, Hkv, max_pages * page_size, device=dev) if track else None
+        self._scores = torch.zeros(layers, rows, Hkv, max_pages * page_size, device=dev) if track else None
+        self._waiting: list = []  # of the step's attend() calls: what moe_kv4_weights takes
+        self._final = False
         self.evicted = torch.zeros_like(self.lens)
         self._evicts = False  # whether evict() was ever called
         # of the step that extend() made room for; None from the call on that moves
@@ -56,17 +59,58 @@ class KV4Cache:
     def _rows(self, rows: Sequence[int]) -> torch.Tensor:
         return torch.tensor(list(rows), dtype=torch.int32, device=self.device)
 
+    @property
+    def scores(self) -> Optional[torch.Tensor]:
+        """fp32 [layers, rows, Hkv, max_pages * page_size]: the sum of the attention
+        weights of each token (None without track).  Read within a step it takes in what
+        the step's attend() calls gave so far, of tokens that are refused later too."""
+        self._sum_up()
+        return self._scores
+
+    @scores.setter
+    def scores(self, scores: Optional[torch.Tensor]) -> None:
+        self._sum_up()
+        self._scores = scores
+
+    def _sum_up(self, refused: Optional[torch.Tensor] = None) -> None:
+        """Adds the weights that wait; those of each row's last refused[row] tokens are left out."""
+        if not self._waiting:
+            return
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("attention weights of attend() calls before this capture wait: read `scores` before it")
+        waiting, self._waiting = self._waiting, []
+        stream, gone = torch.cuda.current_stream(self.device), None
+        for layer, q, lse, step, scale, window, given in waiting:
+            if refused is not None:
+                if gone is None:  # a row's tokens t are those below its end
+                    ends, t = step[0][1:], torch.arange(q.shape[0], dtype=torch.int32, device=self.device)
+                    row = torch.searchsorted(ends, t, right=True).clamp_(max=ends.shape[0] - 1)
+                    gone = (ends[row] - t <= refused[row]).unsqueeze(1)
+                lse.masked_fill_(gone, -torch.inf)
+            if given != stream:
+                for x in (q, lse, *step):
+                    x.record_stream(stream)
+            self._add_weights(layer, q, lse, step, scale, window)
+
+    def _add_weights(self, layer: int, q: torch.Tensor, lse: torch.Tensor, step: tuple, scale: Optional[float], window: int) -> None:
+        api.moe_kv4_weights(q, self.pool[layer], self.g_k[layer], lse, *step, self._scores[layer], scale=scale, window=window)
+
     def _end_step(self) -> None:
+        self._sum_up()
         self.q_offsets = self.slots = self.pos = None
 
-    def extend(self, counts: List[int]) -> None:
+    def extend(self, counts: List[int], final: bool = False) -> None:
         """Room for counts[row] new tokens in each row: sets slots, pos, q_offsets
         and kv_lens for this step.  A row that finds no free page, or has no room
         in its table row, keeps its length; moe_sync_status() reports it, and the
-        step's attention sees no keys for its tokens (zeros)."""
+        step's attention sees no keys for its tokens (zeros).  final: no token of the
+        step will be refused, so that with track=True attend() adds its weights at
+        once; else the rotated queries of all layers are kept until the step ends."""
         rows = self.table.shape[0]
         if len(counts) != rows or min(counts, default=0) < 0:
             raise ValueError(f"counts: expected {rows} numbers of new tokens, one per row, got {list(counts)}")
+        self._sum_up()
+        self._final = final
         offsets = [0, *itertools.accumulate(map(int, counts))]
         q_offsets = torch.tensor(offsets, dtype=torch.int32, device=self.device)
         r = api.moe_kv_extend_ex(q_offsets, offsets[-1], self.table, self.lens, self.refs, self.page_size, inplace=True,
@@ -81,32 +125,43 @@ class KV4Cache:
                interleaved: bool = False, window: int = 0, scale: Optional[float] = None) -> torch.Tensor:
         """The step's tokens through a layer's attention: norms and rotation of q
         and k, k and v into the cache, attention of the rotated queries, and with
-        track=True the weights that it gave to the keys.  q bf16 [T, Hq, D], k and v
-        bf16 [T, Hkv, D] in the order of extend()'s counts.  All layers of a step come
-        before the next call that ends it.  A window counts the tokens that the
-        cache holds, not those that were evicted."""
+        track=True the weights that it gave to the keys, which are added to `scores`
+        when the step ends.  q bf16 [T, Hq, D], k and v bf16 [T, Hkv, D] in the order of
+        extend()'s counts.  All layers of a step come before the next call that ends it.
+        A window counts the tokens that the cache holds, not those that were evicted.
+        In a CUDA graph the weights are added by each replay, those of refused tokens too."""
         if self.q_offsets is None:
             raise ValueError("extend() comes before attend(), and fork(), free() and compact() end its step, as do drop(), "
                              "verify() and evict()")
         pool, g_k, g_v = self.pool[layer], self.g_k[layer], self.g_v[layer]
         q, _ = api.moe_qk_norm_rope(q, k, cos_sin, self.pos, wq=wq, wk=wk, eps=eps, interleaved=interleaved, v=v,
                                     pool=pool, g_k=g_k, g_v=g_v, slots=self.slots)
-        if self.scores is None:
-            return api.moe_kv4_attention(q, pool, g_k, g_v, self.q_offsets, self.kv_lens, self.table, scale=scale, window=window)
+        step = (self.q_offsets, self.kv_lens, self.table)
+        if self._scores is None:
+            return api.moe_kv4_attention(q, pool, g_k, g_v, *step, scale=scale, window=window)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
-        y = api.moe_kv4_attention(q, pool, g_k, g_v, self.q_offsets, self.kv_lens, self.table, scale=scale, window=window, lse=lse)
-        api.moe_kv4_weights(q, pool, g_k, lse, self.q_offsets, self.kv_lens, self.table, self.scores[layer], scale=scale,
-                            window=window)
+        y = api.moe_kv4_attention(q, pool, g_k, g_v, *step, scale=scale, window=window, lse=lse)
+        if self._final or torch.cuda.is_current_stream_capturing():
+            self._add_weights(layer, q, lse, step, scale, window)
+            return y
+        if any(w[0] == layer for w in self._waiting):
+            self._sum_up()
+        # lengths and pages as they are now: the library's calls may change them in place
+        step = self._waiting[0][3] if self._waiting else (step[0], step[1].clone(), step[2].clone())
+        self._waiting.append((layer, q, lse, step, scale, window, torch.cuda.current_stream(self.device)))
         return y
 
     def verify(self, logits: torch.Tensor, tokens: torch.Tensor, u: torch.Tensor, u_next: torch.Tensor,
                draft_probs: Optional[torch.Tensor] = None, temperature: Optional[torch.Tensor] = None) -> dict:
         """The step's drafted tokens against the target's logits (moe_verify_draft, whose
         arguments these are; each row's tokens of the step are the last one that it had
-        and drafted ones), and the refused ones off the rows' ends.  Ends the step.
-        Returns dict(accepted, token, refused), int32 [rows]."""
+        and drafted ones), and the refused ones off the rows' ends, their attention
+        weights with them.  Ends the step.  Returns dict(accepted, token, refused),
+        int32 [rows]."""
         if self.q_offsets is None:
             raise ValueError("extend() and attend() come before verify()")
+        if self._final and self._scores is not None:
+            raise ValueError("verify() may refuse tokens: with track=True not in a step of extend(final=True)")
         r = api.moe_verify_draft(logits, tokens, self.q_offsets, u, u_next, draft_probs=draft_probs, temperature=temperature)
         # a row that found no room does not hold the step's tokens
         self.drop(torch.where(self.kv_lens > 0, r["refused"], 0))
@@ -114,9 +169,13 @@ class KV4Cache:
 
     def drop(self, counts: Union[torch.Tensor, Sequence[int]]) -> None:
         """Each row loses its last counts[row] tokens (int32 [rows], or numbers on the
-        host).  Ends the step."""
-        self._end_step()
+        host).  Ends the step.  The attention weights that tokens of this step gave go
+        with them; those of an earlier step, or of a final one, stay in the sums."""
         counts = counts if isinstance(counts, torch.Tensor) else self._rows(counts)
+        if api._index(counts, "counts", self.device) != self.lens.shape[0]:
+            raise ValueError(f"counts: expected {self.lens.shape[0]} numbers, one per row")
+        self._sum_up(counts)
+        self._end_step()
         api.moe_kv_drop(counts, self.table, self.lens, self.refs, self.pool, self.page_size, inplace=True)
         self._begin_anew()
 
@@ -126,11 +185,11 @@ class KV4Cache:
         so far, in each layer and kv head (needs track=True unless sinks + recent ==
         keep).  The tokens that follow keep counting their positions.  Ends the step.
         Returns the tokens that each row lost, int32 [rows]."""
-        if self.scores is None and sinks + recent != keep:
+        if self._scores is None and sinks + recent != keep:
             raise ValueError("evict() by attention needs a cache with track=True")
         self._end_step()
         self._evicts = True
-        r = api.moe_kv4_evict(self.table, self.lens, self.refs, self.pool, self.scores, keep, limit, sinks, recent, self.D,
+        r = api.moe_kv4_evict(self.table, self.lens, self.refs, self.pool, self._scores, keep, limit, sinks, recent, self.D,
                               inplace=True)
         self.evicted += r["dropped"]
         return r["dropped"]
@@ -138,7 +197,7 @@ class KV4Cache:
     def fork(self, src: Sequence[int], dst: Sequence[int]) -> None:
         """Empty rows dst continue as forks of rows src."""
         self._end_step()
-        if self.scores is not None or self._evicts:
+        if self._scores is not None or self._evicts:
             self._fork_sums(list(src), list(dst))
         api.moe_kv_fork(self._rows(src), self._rows(dst), self.table, self.lens, self.refs, self.pool, self.page_size,
                         inplace=True)
@@ -156,8 +215,8 @@ class KV4Cache:
         d, s = (torch.tensor(list(x), device=self.device) for x in (pairs.keys(), pairs.values()))
         s = torch.where(self.lens[d] == 0, s, d)
         self.evicted[d] = self.evicted[s]
-        if self.scores is not None:
-            self.scores[:, d] = self.scores[:, s]
+        if self._scores is not None:
+            self._scores[:, d] = self._scores[:, s]
 
     def free(self, rows: Sequence[int]) -> None:
         """Rows become empty."""

@@ -126,6 +126,131 @@ def test_refused_tokens_leave_no_trace():
     assert sorted(a.refs.tolist()) == sorted(b.refs.tolist())
 
 
+@pytest.mark.parametrize("by_hand", [False, True])
+def test_refused_tokens_leave_no_trace_in_the_sums(by_hand):
+    """The sums are those of a cache that only ever saw the accepted tokens, and add up to one per
+    query and head of these; whether verify() or the caller's own drop() refuses."""
+    rng = np.random.default_rng(2)
+    V = 50
+    q, k, v, cs = inputs(400)
+    a, b = cache(), cache()
+    at = [60, 33, 0, 64, 95]
+    first = sum(at)
+    for c in (a, b):
+        step(c, at, q[:first], k[:first], v[:first], cs)
+    where, dropped = first, 0
+    for _ in range(6):
+        counts = [int(x) for x in rng.integers(1, 6, ROWS)]
+        counts[2] = 0
+        T = sum(counts)
+        s = slice(where, where + T)
+        where += T
+        step(a, counts, q[s], k[s], v[s], cs)
+        if by_hand:
+            refused = [int(rng.integers(0, max(1, n))) for n in counts]
+            a.drop(refused)
+        else:
+            refused = a.verify(torch.randn(T, V, device="cuda"), torch.from_numpy(rng.integers(0, V, T).astype(np.int32)).cuda(),
+                               torch.rand(T, device="cuda") * 0.05, torch.rand(ROWS, device="cuda"))["refused"].tolist()
+        dropped += sum(refused)
+        took = [n - r for n, r in zip(counts, refused)]
+        starts = np.cumsum([s.start] + counts)
+        rows = [t for i in range(ROWS) for t in range(starts[i], starts[i] + took[i])]
+        step(b, took, q[rows], k[rows], v[rows], cs)
+        assert a.lens.tolist() == b.lens.tolist()
+    assert dropped > 20
+    for row, n in enumerate(a.lens.tolist()):
+        x, y = a.scores[:, row, :, :n], b.scores[:, row, :, :n]
+        # each attention's lse is within 5e-4 of the formula's, and so is every weight
+        assert ((x - y).abs() <= 1.1e-3 * y).all()
+        assert ((x.sum(2) - n * HQ / HKV).abs() <= 1e-3 * n * HQ / HKV).all()
+
+
+def test_sums_wait_for_the_end_of_a_step():
+    q, k, v, cs = inputs(130)
+    a, b, c = cache(), cache(), cache()
+    for s, counts in ((slice(0, 100), [60, 0, 40, 0, 0]), (slice(100, 108), [5, 0, 3, 0, 0])):
+        step(a, counts, q[s], k[s], v[s], cs)
+        step(b, counts, q[s], k[s], v[s], cs)
+        b.scores  # reading takes in what waits
+        c.extend(counts, final=True)
+        for layer in range(LAYERS):
+            c.attend(layer, q[s], k[s], v[s], cs)
+        assert not c._waiting
+    assert len(a._waiting) == LAYERS and not b._waiting
+    assert torch.equal(a.scores, b.scores) and torch.equal(a.scores, c.scores) and not a._waiting
+    # whatever ends the step takes them in first; rows and pages as attention had them
+    for end in (lambda x: x.extend([1] + [0] * 4), lambda x: x.free([0]), lambda x: x.compact(), lambda x: x.fork([0], [1]),
+                lambda x: x.evict(20, sinks=2, recent=5)):
+        one, two = cache(), cache()
+        for x in (one, two):
+            step(x, [60, 0, 40, 0, 0], q[:100], k[:100], v[:100], cs)
+            step(x, [5, 0, 3, 0, 0], q[100:108], k[100:108], v[100:108], cs)
+        two.scores
+        end(one), end(two)
+        assert torch.equal(one._scores, two._scores) and not one._waiting
+    # a layer once more: its first sums are taken in
+    c.extend([1] + [0] * 4)
+    for _ in range(2):
+        c.attend(0, q[108:109], k[108:109], v[108:109], cs)
+    assert len(c._waiting) == 1
+    old = a.scores[0, 0, :, :65].sum()
+    assert abs(float(c.scores[0, 0, :, :66].sum() - old) - 2 * HQ) <= 0.05 * 2 * HQ
+    c.extend([1] + [0] * 4, final=True)
+    with pytest.raises(ValueError, match="final"):
+        c.verify(torch.zeros(1, 4, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, device="cuda"),
+                 torch.zeros(ROWS, device="cuda"))
+    for bad in ([1, 2], torch.zeros(4, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError, match="counts"):
+            c.drop(bad)
+    assert c.q_offsets is not None
+
+
+def test_sums_of_another_stream_and_of_a_graph():
+    q, k, v, cs = inputs(80)
+    a, b = cache(), cache()
+    for c in (a, b):
+        step(c, [70, 0, 0, 0, 0], q[:70], k[:70], v[:70], cs)
+    base = a.scores.clone()
+    assert torch.equal(base, b.scores)
+    side = torch.cuda.Stream()
+    step(a, [2, 0, 0, 0, 0], q[70:72], k[70:72], v[70:72], cs)
+    b.extend([2, 0, 0, 0, 0])
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for layer in range(LAYERS):
+            b.attend(layer, q[70:72], k[70:72], v[70:72], cs)
+    torch.cuda.current_stream().wait_stream(side)
+    a.drop([1, 0, 0, 0, 0]), b.drop([1, 0, 0, 0, 0])
+    assert torch.equal(a.scores[:, :, :, :71], b.scores[:, :, :, :71])
+    # a replay adds the weights of its step each time
+    before = a.scores.clone()
+    a.extend([1, 0, 0, 0, 0])
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        for layer in range(LAYERS):
+            a.attend(layer, q[72:73], k[72:73], v[72:73], cs)
+    assert not a._waiting
+    for n in (1, 2):
+        graph.replay()
+        gave = a.scores[:, 0, :, :71] - before[:, 0, :, :71]
+        last = a.scores[:, 0, :, 71]
+        assert ((gave.sum(2) / n + last - HQ / HKV).abs() <= 2e-3 * HQ / HKV).all()
+    # sums that wait are not caught by a capture
+    b.extend([1, 0, 0, 0, 0])
+    b.attend(0, q[72:73], k[72:73], v[72:73], cs)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(ValueError, match="capture"):
+        with torch.cuda.graph(graph):
+            b.evict(40)
+    assert len(b._waiting) == 1
+    torch.cuda.synchronize()
+    b.evict(40)
+    assert b.lens.tolist() == [40, 0, 0, 0, 0]
+
+
 def test_rows_that_found_no_room_lose_nothing():
     import mixture_experts_layer_fwd_gb300 as m
     q, k, v, cs = inputs(200)
