@@ -551,7 +551,7 @@ def moe_linear_nvfp4(x: torch.Tensor, codes: torch.Tensor, sf: torch.Tensor, g: 
                      add: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                      out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Up to 32 tokens times a matrix in NVFP4 (see include/moe_gb300.h): x bf16
-    [T, K] (any row stride), codes uint8 [N, K/2], sf uint8 [N, K/16], g fp32 [1]
+    [T, K] (rows on 16-byte boundaries), codes uint8 [N, K/2], sf uint8 [N, K/16], g fp32 [1]
     as moe_quant_nvfp4 gives them; add bf16 [T, N] (any row stride) is added
     before the one rounding.  Returns out [T, N], bf16 or fp32."""
     try:

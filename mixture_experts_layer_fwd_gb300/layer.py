@@ -29,10 +29,13 @@ class NVFP4Tensor:
         [T, rows]: moe_linear_nvfp4 for up to 32 tokens.  More go through
         moe_grouped_gemm as one group (the product is then rounded to bf16 before
         the sum), and 32 at a time through moe_linear_nvfp4 where fp32 is asked for
-        or the matrix is none of moe_grouped_gemm's (rows % 32, cols % 64)."""
+        or the matrix is none of moe_grouped_gemm's (rows % 32, cols % 64).  Tokens
+        that do not lie on 16-byte boundaries are copied."""
         N, K = self.codes.shape[-2], self.codes.shape[-1] * 2
         codes, sf = self.codes.view(N, K // 2), self.sf.view(N, K // 16)
         T = x.shape[0]
+        if x.data_ptr() % 16 or (T > 1 and x.stride(0) % 8):
+            x = x.clone(memory_format=torch.contiguous_format)
         if T <= 32:
             return api.moe_linear_nvfp4(x, codes, sf, self.g, add=add, out_dtype=out_dtype)
         x = x.contiguous()

@@ -390,6 +390,20 @@ def test_a_quantised_matrix_gives_fp32_sums_for_any_number_of_tokens(rows, cols)
             w.linear(x[:64], add=bad, out_dtype=torch.float32)
 
 
+@pytest.mark.parametrize("T", [1, 7, 40])
+def test_a_quantised_matrix_takes_tokens_wherever_they_lie(T):
+    import mixture_experts_layer_fwd_gb300 as m
+    g = torch.Generator("cuda").manual_seed(3)
+    w = m.quantize_weights((torch.randn(96, 256, generator=g, device="cuda") / 16).bfloat16())
+    x = torch.randn(T, 256, generator=g, device="cuda").bfloat16()
+    want = [w.linear(x), w.linear(x, out_dtype=torch.float32)]
+    for more, at in ((4, 0), (8, 4), (3, 1)):
+        wide = torch.zeros(T, 256 + more, dtype=torch.bfloat16, device="cuda")
+        wide[:, at:at + 256] = x
+        y = wide[:, at:at + 256]
+        assert torch.equal(w.linear(y), want[0]) and torch.equal(w.linear(y, out_dtype=torch.float32), want[1])
+
+
 def test_speculative_decoding_example_runs():
     r = subprocess.run([sys.executable, os.path.join(ROOT, "examples", "speculative_decoding.py")], capture_output=True, text=True,
                        timeout=300)
