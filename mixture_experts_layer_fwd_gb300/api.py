@@ -1082,7 +1082,8 @@ def moe_kv4_evict(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, p
         if score.dim() != 4 or score.shape[:3] != (layers, S, Hkv) or score.shape[3] < M * page_size:
             raise ValueError(f"score: expected [{layers}, {S}, {Hkv}, >= {M * page_size}], got {tuple(score.shape)}")
         cap = score.shape[3]
-    limit = keep if limit is None else limit
+    # more tokens than any row has; ctypes would cut such numbers off silently
+    keep, limit, sinks, recent = (max(-1, min(n, _INT_MAX)) for n in (keep, keep if limit is None else limit, sinks, recent))
     o = out or {}
     r = dict(table=_like(o.get("table"), "table", table, inplace, stream),
              lens=_like(o.get("lens"), "lens", lens, inplace, stream),
@@ -1092,7 +1093,7 @@ def moe_kv4_evict(table: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, p
     ws = _empty(lib.moe_kv4_evict_workspace_size(layers, S, M, N, Hkv, max(keep, 1)), _U8, dev, stream)
     check(lib.moe_kv4_evict(_ptr(table), _ptr(lens), _ptr(refs), S, M, N, page_size, _ptr(r["table"]), _ptr(r["lens"]),
                             _ptr(r["refs"]), _ptr(r["dropped"]), _ptr(pool), layers, N * Hkv * record, Hkv, D, _ptr(score), cap,
-                            keep, min(limit, _INT_MAX), sinks, recent, _ptr(ws), ws.numel(), _raw_stream(stream, table)),
+                            keep, limit, sinks, recent, _ptr(ws), ws.numel(), _raw_stream(stream, table)),
           "moe_kv4_evict")
     return r
 

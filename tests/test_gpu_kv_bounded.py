@@ -74,6 +74,23 @@ def test_what_stays_after_eviction_is_what_attention_looked_at(n):
         c.attend(0, q[:1], k[:1], v[:1], cs)
 
 
+def test_numbers_past_32_bits_evict_nothing():
+    import mixture_experts_layer_fwd_gb300 as m
+    q, k, v, cs = inputs(100)
+    c = cache()
+    step(c, [100, 0, 0, 0, 0], q, k, v, cs)
+    before = bytes_of(c, 0, 100)
+    for kw in (dict(keep=2 ** 32 + 8), dict(keep=2 ** 32 + 8, limit=2 ** 32 + 9, sinks=2, recent=3), dict(keep=50, limit=2 ** 40 + 60),
+               dict(keep=2 ** 63, sinks=4)):
+        assert c.evict(**kw).tolist() == [0] * ROWS and c.lens.tolist()[0] == 100
+    for kw in (dict(keep=60, sinks=2 ** 32), dict(keep=60, recent=2 ** 32 + 1), dict(keep=-2 ** 32 + 60, limit=100),
+               dict(keep=60, limit=2 ** 32 - 2 ** 33 + 80)):
+        with pytest.raises(m._lib.MoEError, match="INVALID"):
+            c.evict(**kw)
+    for x, y in zip(before, bytes_of(c, 0, 100)):
+        assert torch.equal(x, y)
+
+
 def test_positions_go_on_after_eviction_and_attention_sees_what_stayed():
     import mixture_experts_layer_fwd_gb300 as m
     q, k, v, cs = inputs(130)
