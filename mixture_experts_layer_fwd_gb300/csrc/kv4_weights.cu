@@ -646,7 +646,7 @@ DEVINL void many_rows(const Params& p, Stage<D>& sh) {
 //             columns
 //   8         bulk copies of tiles of rows and of what their columns need
 //   9, 10     issue the matrix instructions for the first and the second four: what one
-//             waits for is hidden under the other's (one for both 1.15 against 0.73 ms)
+//             waits for is hidden under the other's (one for both 1150 against 878 us on the long chunk)
 //   11        takes items (sequence, kv head, keys) and publishes them, one ahead
 //   12-15     expand the next item's keys into the swizzle that the instructions read
 //

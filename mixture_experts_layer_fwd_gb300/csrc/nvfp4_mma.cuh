@@ -20,13 +20,6 @@ DEVINL void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, ui
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four E4M3 bytes -> four fp16 pairs, both halves the same.
-DEVINL void e4m3x4_pairs(uint32_t s, uint32_t (&f)[4]) {
-  const uint32_t lo = e4m3x2_to_f16x2(s & 0xFFFFu), hi = e4m3x2_to_f16x2(s >> 16);
-  f[0] = __byte_perm(lo, lo, 0x1010), f[1] = __byte_perm(lo, lo, 0x3232);
-  f[2] = __byte_perm(hi, hi, 0x1010), f[3] = __byte_perm(hi, hi, 0x3232);
-}
-
 // One word of codes of matrix rows g and g + 8, times their scales.
 struct Expanded {
   uint32_t a[4], b[4];
