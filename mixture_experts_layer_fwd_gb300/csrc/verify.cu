@@ -17,7 +17,7 @@
 //
 // 64 sequences of up to seven drafts, 151936 words, bf16: 20 + 32 us on the GPU (the first
 // launch 4.1 TB/s of the logits; the second 68 instructions per value, 0.38 of the issue
-// slots, since it begins and ends with chains of dependent loads).  One sequence of four drafts: 4 + 14 us, the call with moe_kv_drop 42.
+// slots, since it begins and ends with chains of dependent loads).  One sequence of four drafts: 4 + 14 us, the call with moe_kv_drop 43 - 46.
 #include "kv4_attention.cuh"
 
 namespace moe {
