@@ -12,7 +12,7 @@
 //   up to 16    every warp takes an equal range of the line of all (sequence, kv head,
 //               32 keys), holds the rows' operands in registers and streams the keys
 //               through a ring of asynchronous copies
-//   up to 127   a block takes 32 to 128 keys, expands them into registers and walks the
+//   up to 255   a block takes 32 to 128 keys, expands them into registers and walks the
 //               rows that see one of them, staged 32 KB at a time
 //   more        tcgen05, in a launch of its own (see there)
 // A key's rows are added in a fixed order: the same result each time.
@@ -32,10 +32,12 @@ namespace {
 
 constexpr int kKeys = 32;         // of a warp's step
 constexpr int kFewRows = 16;      // of a sequence and kv head: a warp holds them in registers
-// These and more go to the tiles' kernel: 32 sequences of 8192 keys, heads of 128, 64 /
-// 128 / 192 / 512 rows 156 / 140 / 187 / 206 us there, 119 / 153 / 195 / 407 in registers;
-// 16 of 4096 keys, heads of 64, 64 / 128 / 512 rows 82 / 73 / 101 and 57 / 69 / 145.
-constexpr int kTileRows = 128;
+// These and more go to the tiles' kernel: 32 sequences of 8192 keys, heads of 128, 128 /
+// 192 / 256 / 384 / 512 rows 178 / 217 / 194 / 218 / 231 us on the GPU there, 149 / 189 /
+// 226 / 311 / 395 in registers; of up to 8192 keys 78 / 96 / 108 / 123 / 140 and 69 / 82 /
+// 97 / 124 / 154; 16 of 4096 keys, heads of 64, 128 / 256 / 384 / 512 rows 44 / 49 / 56 / 60
+// and 35 / 47 / 62 / 74.
+constexpr int kTileRows = 256;
 constexpr int kTileKeys = 128;    // of an item there
 constexpr int kParts = 4;         // of an item, where they are few
 constexpr int kPrepThreads = 256, kThreads = 256;

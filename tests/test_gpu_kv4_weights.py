@@ -119,7 +119,7 @@ def test_weights_of_few_rows_among_many_empty_sequences(D, G):
 
 
 @pytest.mark.parametrize("D,Hkv,G,qs,kvs", [(128, 4, 3, [120, 125], [4800, 5200]),   # 3 tiles of 128 rows to an item
-                                            (128, 4, 2, [190, 65], [3000, 7000]),    # 3; 2
+                                            (128, 4, 2, [190, 128], [3000, 7000]),   # 3; 2
                                             (64, 4, 3, [120, 210], [6000, 3000])])   # 3; 5
 def test_weights_of_items_with_an_odd_number_of_tiles(D, Hkv, G, qs, kvs):
     """Several items to a block: a slot of the rings holds tiles of either place in an item."""
