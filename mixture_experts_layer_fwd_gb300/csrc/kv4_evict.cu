@@ -13,9 +13,9 @@
 // them in place, 256 at a time: what one step writes, no later step reads.
 //
 // 32 conversations of 4096 tokens, 1500 of which stay, 32 layers, 4 heads of 128: 5 + 56 +
-// 262 us with nothing in L2 (the move at 5.1 TB/s of both ways, 0.8 of DRAM's cycles), 279 to
-// 304 us with the call after itself, by the GPU.  One conversation of 1300 tokens, 4 layers: 9 + 10 us, the call
-// 27 (33 with a plan in front).
+// 262 us with nothing in L2 (the move at 5.1 TB/s of both ways, 0.8 of DRAM's cycles), 261 to
+// 304 us with the call after itself, by the GPU.  One conversation of 1300 tokens, 4 layers:
+// 9 + 10 us, the call 27 (33 with a plan in front).
 #include "kv4.cuh"
 
 namespace moe {
